@@ -75,8 +75,11 @@ typedef enum {
     W4A8_EWORKSPACE = 4     /* the caller's workspace is smaller than the call needs */
 } w4a8_status;
 
-#define W4A8_ABI_VERSION 6
+#define W4A8_ABI_VERSION 7
 #define W4A8_GROUP 128
+
+/* Element types of the entry points that take more than fp32. */
+typedef enum { W4A8_F32 = 0, W4A8_F16 = 1, W4A8_BF16 = 2 } w4a8_dtype;
 
 int w4a8_abi_version(void);
 const char *w4a8_status_str(int status);
@@ -262,6 +265,42 @@ w4a8_status w4a8_gemm_tm(const int8_t *qa, const float *a_scale, int64_t M, int6
                          const uint8_t *tm, int64_t N, int32_t group, float *out,
                          hipStream_t stream);
 
+/* ------------------------------------------------------------ 8-bit weights
+ * Layers whose weights keep 8 bits: INT8 codes with one scale per output channel
+ * ([p3 §2.3]: per-token activations, per-channel weights), row-major qw[N][K] and
+ * w_scale[N].  w4a8_quantize_act run over the rows of W[N][K] makes both (its scale
+ * per row is then the channel's), w4a8_quantize_act_smooth with the factors s the
+ * smoothed form. */
+
+/* Device.  out[m][n] = T(fp32(isum) * a_scale[m] * w_scale[n] + bias[n]) with
+ *     isum = sum_k qa[m][k] * qw[n][k]   (int32, exact)
+ * the products and the sum in fp32, in that order, and one rounding to the output's
+ * type T (out_type: W4A8_F32, W4A8_F16 or W4A8_BF16; values past the type's range
+ * become infinities).  bias: fp32 [N] or NULL.  Row m of out starts at element
+ * m * ldo, ldo >= N; the elements between rows are not written.  The output bytes do
+ * not depend on M: a row gives the same bytes alone as in a batch.
+ * Any M >= 0 and N > 0; K a positive multiple of 16 below 131072 (the int32 sum
+ * cannot overflow).  qa and qw 16-byte aligned, out aligned to its element.
+ * Errors: W4A8_EINVAL (null, bad sizes, ldo < N, misalignment), W4A8_EUNSUPPORTED
+ * (another out_type).  M == 0 is a no-op. */
+w4a8_status w4a8_gemm_w8a8(const int8_t *qa, const float *a_scale, int64_t M, int64_t K,
+                           const int8_t *qw, const float *w_scale, int64_t N, const float *bias,
+                           void *out, int32_t out_type, int64_t ldo, hipStream_t stream);
+
+/* Device.  Expert-grouped form: slot s in [expert_offsets[e], expert_offsets[e+1])
+ * multiplies activation row row_index[s] (NULL: row s) with expert e's weights and
+ * writes out[s][0..N) (fp32).  qa [R][K], a_scale [R], qw [E][N][K],
+ * w_scale [E][N], out [max_slots][N]; arithmetic, K and N as w4a8_gemm_w8a8, the
+ * slot lists as w4a8_moe_grouped_gemm (they stay on the device; offsets are clamped
+ * to [0, max_slots], and slots whose row_index is outside [0, R) and slots of no
+ * expert are not written).  1 <= E <= 1024.
+ * Errors: W4A8_EINVAL (null, bad sizes, qa, qw or out not 16-byte aligned).
+ * max_slots == 0 or R == 0 is a no-op. */
+w4a8_status w4a8_moe_grouped_gemm_w8a8(const int8_t *qa, const float *a_scale, int64_t R,
+                                       const int32_t *row_index, const int32_t *expert_offsets,
+                                       int32_t E, int64_t K, const int8_t *qw, const float *w_scale,
+                                       int64_t N, int64_t max_slots, float *out, hipStream_t stream);
+
 /* ---------------------------------------------------------------------- MoE */
 
 /* Device.  Router for T tokens over E experts ([p1 §5.2]: the router stays in
@@ -287,6 +326,39 @@ w4a8_status w4a8_moe_route(const float *logits, int64_t T, int32_t E, int32_t to
                            int32_t with_shared, int32_t *topk_ids, float *topk_w,
                            int32_t *expert_offsets, int32_t *perm, int32_t *slot_row,
                            int32_t *slot_of_pair, hipStream_t stream);
+
+/* Device.  Router by scores, for models whose picks are not the plain top-k of the
+ * logits; it writes the same tables as w4a8_moe_route.  With x = logits[t][e] (NaN
+ * counts as -inf, values above the largest fp32 as that):
+ *   s   = 1 / (1 + exp(-x)) (score W4A8_SCORE_SIGMOID) or the softmax of the token's
+ *         logits (W4A8_SCORE_SOFTMAX); 0 where x is -inf
+ *   v   = s + bias[e], or s without a bias; the picks' order goes by key = v, or by x
+ *         itself without a bias.  bias: fp32 [E] or NULL, NaN counting as -inf.  An
+ *         expert whose logit or bias is -inf has v = key = -inf
+ *   the E experts form n_groups runs of E / n_groups; a group's value is the sum of
+ *         its group_lead (1 or 2) largest v, and only the topk_groups groups of the
+ *         largest values stay (ties: the lower group).  n_groups = 1 takes all
+ *   topk_ids[T][k]  the k largest keys of what is left, descending, ties -> lower id
+ *   topk_w[T][k]    s of each pick (0 if its key is -inf), with renorm = 1 divided by
+ *                   the sum over the token's picks (all 0 if that is 0), times scale
+ * Scores, keys and their sums are taken in fp64 and the weight is rounded once to
+ * fp32, so that picks do not turn on fp32 rounding.  The bias steers the choice only.
+ * Every token gets k distinct ids in [0, E) whatever its logits hold.
+ * logits: device [T][E] of logits_type (W4A8_F32, W4A8_F16, W4A8_BF16), row stride
+ * ldl >= E elements.  The tables, with_shared and T == 0 are as in w4a8_moe_route
+ * (slot_row may be NULL).  Requires 1 <= E <= 1024, 1 <= k <= min(E, 32),
+ * T * (k + 1) < 2^31, n_groups in [1, 64] dividing E, 1 <= topk_groups <= n_groups,
+ * k <= topk_groups * E / n_groups, group_lead <= E / n_groups, a finite scale.
+ * Errors: W4A8_EINVAL (null, bad values), W4A8_EUNSUPPORTED (another logits_type or
+ * score). */
+#define W4A8_SCORE_SOFTMAX 0
+#define W4A8_SCORE_SIGMOID 1
+w4a8_status w4a8_moe_route_scored(const void *logits, int32_t logits_type, int64_t ldl, const float *bias,
+                                  int64_t T, int32_t E, int32_t topk, int32_t with_shared, int32_t score,
+                                  int32_t n_groups, int32_t topk_groups, int32_t group_lead, int32_t renorm,
+                                  float scale, int32_t *topk_ids, float *topk_w, int32_t *expert_offsets,
+                                  int32_t *perm, int32_t *slot_row, int32_t *slot_of_pair,
+                                  hipStream_t stream);
 
 /* Device.  Expert-grouped W4A8 GEMM.  Slots s in [expert_offsets[e],
  * expert_offsets[e+1]) belong to expert e; slot s multiplies activation row

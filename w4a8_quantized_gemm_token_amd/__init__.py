@@ -16,7 +16,7 @@ import os
 import numpy as np
 
 GROUP = 128
-ABI_VERSION = 6          # W4A8_ABI_VERSION of the header this binding follows
+ABI_VERSION = 7          # W4A8_ABI_VERSION of the header this binding follows
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libw4a8.so")
 
@@ -27,6 +27,7 @@ EXPORTS = (
     "w4a8_quantize_act", "w4a8_gemm", "w4a8_gemm_debug_isums", "w4a8_gemm_path",
     "w4a8_tm_bytes", "w4a8_weights_to_tm", "w4a8_gemm_tm",
     "w4a8_channel_absmax", "w4a8_smooth_factors", "w4a8_pack_weights_device_smooth", "w4a8_quantize_act_smooth",
+    "w4a8_gemm_w8a8", "w4a8_moe_grouped_gemm_w8a8", "w4a8_moe_route_scored",
     "w4a8_moe_route", "w4a8_moe_grouped_gemm", "w4a8_moe_grouped_gemm_debug_isums", "w4a8_silu_mul_quantize",
     "w4a8_moe_combine",
     "w4a8_moe_ffn_workspace_size", "w4a8_moe_ffn_workspace_layout", "w4a8_moe_ffn",
@@ -75,6 +76,10 @@ def load() -> ctypes.CDLL:
         "w4a8_weights_to_tm": (ctypes.c_int, [p, p, p, i64, i64, i32, p, p]),
         "w4a8_gemm_tm": (ctypes.c_int, [p, p, i64, i64, p, i64, i32, p, p]),
         "w4a8_moe_route": (ctypes.c_int, [p, i64, i32, i32, i32, p, p, p, p, p, p, p]),
+        "w4a8_moe_route_scored": (ctypes.c_int, [p, i32, i64, p, i64, i32, i32, i32, i32, i32, i32, i32, i32,
+                                                 ctypes.c_float, p, p, p, p, p, p, p]),
+        "w4a8_gemm_w8a8": (ctypes.c_int, [p, p, i64, i64, p, p, i64, p, p, i32, i64, p]),
+        "w4a8_moe_grouped_gemm_w8a8": (ctypes.c_int, [p, p, i64, p, p, i32, i64, p, p, i64, i64, p, p]),
         "w4a8_moe_grouped_gemm": (ctypes.c_int, [p, p, i64, p, p, i32, i64, p, p, p, i64, i32, i64, p, p]),
         "w4a8_moe_grouped_gemm_debug_isums": (ctypes.c_int, [p, i64, p, p, i32, i64, p, p, i64, i32, i64, p, p]),
         "w4a8_silu_mul_quantize": (ctypes.c_int, [p, i64, i64, p, p, p, p]),
@@ -366,6 +371,63 @@ def prepare_gemm_tm(qa, a_scale, tm, out, group: int = GROUP) -> Launch:
                                    _stream(qa.device)), (qa, a_scale, tm, out))
 
 
+# ----------------------------------------------------------------- 8-bit weights
+def _dtype_code(dtype) -> int:
+    torch = _torch()
+    codes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # w4a8_dtype
+    assert dtype in codes, "float32, float16 or bfloat16 expected"
+    return codes[dtype]
+
+
+def _same_device(*tensors):
+    assert len({t.device for t in tensors if t is not None}) == 1, "all tensors must be on one device"
+
+
+def _is(t, shape, dtype, what):
+    assert t is None or (tuple(t.shape) == tuple(shape) and t.dtype == dtype), f"{what}: {dtype} {tuple(shape)} expected"
+
+
+def quantize_weights_w8(W):
+    """W float32 [N][K] (device) -> (qw int8 [N][K], w_scale float32 [N]): symmetric 8-bit codes per
+    output channel, which is the row quantizer of the activations run over W's rows."""
+    return quantize_act(W)
+
+
+def _gemm_w8a8_args(qa, a_scale, qw, w_scale, bias, out):
+    torch = _torch()
+    M, K = qa.shape
+    N = qw.shape[0]
+    _is(qa, (M, K), torch.int8, "qa")
+    _is(a_scale, (M,), torch.float32, "a_scale")
+    _is(qw, (N, K), torch.int8, "qw")
+    _is(w_scale, (N,), torch.float32, "w_scale")
+    _is(bias, (N,), torch.float32, "bias")
+    assert tuple(out.shape) == (M, N), "out: [M][N] expected"
+    _same_device(qa, a_scale, qw, w_scale, bias, out)
+    ldo = out.stride(0) if M > 1 else max(N, 1)
+    return (_dev_ptr(qa), _dev_ptr(a_scale), M, K, _dev_ptr(qw), _dev_ptr(w_scale), N, _dev_ptr(bias),
+            _dev_rows_ptr(out), _dtype_code(out.dtype), ldo, _stream(qa.device))
+
+
+def gemm_w8a8(qa, a_scale, qw, w_scale, bias=None, out_dtype=None, out=None):
+    """out [M][N] = 8-bit product of the quantized activations qa [M][K] and weights qw [N][K], scaled per
+    token and output channel, plus bias float32 [N].  out_dtype: float32 (default), float16 or bfloat16;
+    a given `out` may have strided rows."""
+    torch = _torch()
+    if out is None:
+        out = _empty((qa.shape[0], qw.shape[0]), out_dtype or torch.float32, qa)
+    assert out_dtype is None or out.dtype == out_dtype
+    with torch.cuda.device(qa.device):
+        _call("w4a8_gemm_w8a8", *_gemm_w8a8_args(qa, a_scale, qw, w_scale, bias, out))
+    return out
+
+
+def prepare_gemm_w8a8(qa, a_scale, qw, w_scale, out, bias=None) -> Launch:
+    """Prepared w4a8_gemm_w8a8 writing into a preallocated out [M][N] (float32, float16 or bfloat16)."""
+    return Launch("w4a8_gemm_w8a8", _gemm_w8a8_args(qa, a_scale, qw, w_scale, bias, out),
+                  (qa, a_scale, qw, w_scale, bias, out))
+
+
 def linear(x, packed, scale, zp, path: int = 0):
     """Quantize x per token and run the W4A8 product: float32 [M][N]."""
     qa, sc = quantize_act(x)
@@ -403,6 +465,94 @@ def moe_grouped_gemm(qa, a_scale, row_index, offsets, packed, scale, zp, max_slo
           E, K, _dev_ptr(packed), _dev_ptr(scale), _dev_ptr(zp), N, group, max_slots, _dev_ptr(out),
           _stream(qa.device))
     return out
+
+
+SCORES = {"softmax": 0, "sigmoid": 1}  # W4A8_SCORE_*
+
+
+def _route_scored_args(logits, topk, outs, bias, score, n_groups, topk_groups, group_lead, renorm, scale, with_shared):
+    torch = _torch()
+    T, E = logits.shape
+    sh = 1 if with_shared else 0
+    ids, w, off, perm, rows, sop = outs
+    _is(bias, (E,), torch.float32, "bias")
+    _is(ids, (T, topk), torch.int32, "ids")
+    _is(w, (T, topk), torch.float32, "w")
+    _is(off, (E + 1 + sh,), torch.int32, "offsets")
+    _is(perm, (T * topk,), torch.int32, "perm")
+    _is(rows, (T * topk + sh * T,), torch.int32, "row_index")
+    _is(sop, (T * topk,), torch.int32, "slot_of_pair")
+    assert score in SCORES, f"score: one of {sorted(SCORES)} expected"
+    _same_device(logits, bias, *outs)
+    ldl = logits.stride(0) if T > 1 else E
+    return (_dev_rows_ptr(logits), _dtype_code(logits.dtype), ldl, _dev_ptr(bias), T, E, topk, sh, SCORES[score],
+            n_groups, topk_groups, group_lead, 1 if renorm else 0, float(scale), _dev_ptr(ids), _dev_ptr(w),
+            _dev_ptr(off), _dev_ptr(perm), _dev_ptr(rows), _dev_ptr(sop), _stream(logits.device))
+
+
+def moe_route_scored(logits, topk: int, bias=None, score: str = "softmax", n_groups: int = 1, topk_groups: int = 1,
+                     group_lead: int = 1, renorm: bool = True, scale: float = 1.0, with_shared: bool = False):
+    """Router by softmax or sigmoid scores: picks by score + bias among the topk_groups best of n_groups expert
+    groups (each valued by the sum of its group_lead best), weights = scores of the picks, renormalised and
+    scaled.  logits [T][E] float32, float16 or bfloat16 (rows may be strided), bias float32 [E].
+    Returns the tables of moe_route."""
+    torch = _torch()
+    T, E = logits.shape
+    sh = 1 if with_shared else 0
+    outs = (_empty((T, topk), torch.int32, logits), _empty((T, topk), torch.float32, logits),
+            _empty((E + 1 + sh,), torch.int32, logits), _empty((T * topk,), torch.int32, logits),
+            _empty((T * topk + sh * T,), torch.int32, logits), _empty((T * topk,), torch.int32, logits))
+    with torch.cuda.device(logits.device):
+        _call("w4a8_moe_route_scored", *_route_scored_args(logits, topk, outs, bias, score, n_groups, topk_groups,
+                                                           group_lead, renorm, scale, with_shared))
+    return outs
+
+
+def prepare_moe_route_scored(logits, topk: int, outs, bias=None, score: str = "softmax", n_groups: int = 1,
+                             topk_groups: int = 1, group_lead: int = 1, renorm: bool = True, scale: float = 1.0,
+                             with_shared: bool = False) -> Launch:
+    """Prepared w4a8_moe_route_scored into outs = (ids, w, offsets, perm, row_index, slot_of_pair), shaped as
+    moe_route_scored returns them."""
+    return Launch("w4a8_moe_route_scored", _route_scored_args(logits, topk, outs, bias, score, n_groups, topk_groups,
+                                                              group_lead, renorm, scale, with_shared),
+                  (logits, bias) + tuple(outs))
+
+
+def _grouped_w8a8_args(qa, a_scale, row_index, offsets, qw, w_scale, max_slots, out):
+    torch = _torch()
+    R, K = qa.shape
+    E, N = qw.shape[0], qw.shape[1]
+    _is(qa, (R, K), torch.int8, "qa")
+    _is(a_scale, (R,), torch.float32, "a_scale")
+    _is(qw, (E, N, K), torch.int8, "qw")
+    _is(w_scale, (E, N), torch.float32, "w_scale")
+    _is(out, (max_slots, N), torch.float32, "out")
+    assert offsets.dtype == torch.int32 and offsets.numel() > E, "offsets: int32 [E+1] expected"
+    assert row_index is None or (row_index.dtype == torch.int32 and row_index.numel() >= max_slots), \
+        "row_index: int32 [max_slots] expected"
+    assert row_index is not None or R >= max_slots, "without row_index, qa has a row per slot"
+    _same_device(qa, a_scale, row_index, offsets, qw, w_scale, out)
+    return (_dev_ptr(qa), _dev_ptr(a_scale), R, _dev_ptr(row_index), _dev_ptr(offsets), E, K, _dev_ptr(qw),
+            _dev_ptr(w_scale), N, max_slots, _dev_ptr(out), _stream(qa.device))
+
+
+def moe_grouped_gemm_w8a8(qa, a_scale, row_index, offsets, qw, w_scale, max_slots: int, out=None):
+    """Expert-grouped 8-bit product: out[s] = qa[row_index[s]] times the weights qw [E][N][K] of slot s's expert,
+    scaled per token and per expert channel (w_scale [E][N]); float32 [max_slots][N]."""
+    torch = _torch()
+    if out is None:
+        out = _empty((max_slots, qw.shape[1]), torch.float32, qa)
+    with torch.cuda.device(qa.device):
+        _call("w4a8_moe_grouped_gemm_w8a8",
+              *_grouped_w8a8_args(qa, a_scale, row_index, offsets, qw, w_scale, max_slots, out))
+    return out
+
+
+def prepare_moe_grouped_gemm_w8a8(qa, a_scale, row_index, offsets, qw, w_scale, max_slots: int, out) -> Launch:
+    """Prepared w4a8_moe_grouped_gemm_w8a8 writing into a preallocated out float32 [max_slots][N]."""
+    return Launch("w4a8_moe_grouped_gemm_w8a8",
+                  _grouped_w8a8_args(qa, a_scale, row_index, offsets, qw, w_scale, max_slots, out),
+                  (qa, a_scale, row_index, offsets, qw, w_scale, out))
 
 
 def moe_grouped_gemm_debug_isums(qa, row_index, offsets, packed, zp, max_slots: int, group: int = GROUP):

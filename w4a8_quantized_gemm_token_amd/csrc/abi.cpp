@@ -15,7 +15,7 @@
 #include <thread>
 #include <vector>
 
-#include "w4a8_internal.hpp"
+#include "w8_internal.hpp"
 
 namespace w4a8 {
 
@@ -451,6 +451,89 @@ w4a8_status w4a8_moe_grouped_gemm_debug_isums(const int8_t *qa, int64_t R, const
     return hip_status(launch_grouped_gemm(qa, nullptr, R, row_index, expert_offsets, E, K, packed, nullptr, zp, N,
                                           max_slots, max_slots, nullptr, isums, group, stream),
                       "grouped_gemm_debug_isums launch");
+}
+
+// K of the 8-bit product: whole 16-byte chunks, and |sum| <= 2^14 K < 2^31
+static w4a8_status check_w8(int64_t K, int64_t N) {
+    W4A8_REQUIRE(K > 0 && K % 16 == 0 && K < (1ll << 17), W4A8_EINVAL,
+                 "K=%lld must be a positive multiple of 16 below 131072", (long long)K);
+    W4A8_REQUIRE(N > 0 && N < (1ll << 31), W4A8_EINVAL, "N=%lld must be in [1, 2^31)", (long long)N);
+    return W4A8_OK;
+}
+
+w4a8_status w4a8_gemm_w8a8(const int8_t *qa, const float *a_scale, int64_t M, int64_t K, const int8_t *qw,
+                           const float *w_scale, int64_t N, const float *bias, void *out, int32_t out_type,
+                           int64_t ldo, hipStream_t stream) {
+    clear_error();
+    W4A8_REQUIRE(qw && w_scale && (M == 0 || (qa && a_scale && out)), W4A8_EINVAL, "null pointer");
+    if (w4a8_status st = check_w8(K, N)) return st;
+    W4A8_REQUIRE(M >= 0 && M < (1ll << 31), W4A8_EINVAL, "M=%lld must be in [0, 2^31)", (long long)M);
+    W4A8_REQUIRE(ldo >= N, W4A8_EINVAL, "ldo=%lld must be at least N=%lld", (long long)ldo, (long long)N);
+    W4A8_REQUIRE(out_type == W4A8_F32 || out_type == W4A8_F16 || out_type == W4A8_BF16, W4A8_EUNSUPPORTED,
+                 "out_type=%d is not a supported type", (int)out_type);
+    W4A8_REQUIRE(aligned16(qa) && aligned16(qw), W4A8_EINVAL, "qa and qw must be 16-byte aligned");
+    W4A8_REQUIRE(((uintptr_t)out & (out_type == W4A8_F32 ? 3u : 1u)) == 0, W4A8_EINVAL,
+                 "out must be aligned to its element");
+    W4A8_REQUIRE(((M + 15) / 16) * ((N + 15) / 16) < (1ll << 31), W4A8_EINVAL, "M*N too large");
+    if (M == 0) return W4A8_OK;
+    return hip_status(launch_gemm_w8a8(qa, a_scale, M, K, qw, w_scale, N, bias, out, out_type, ldo, stream),
+                      "gemm_w8a8 launch");
+}
+
+w4a8_status w4a8_moe_grouped_gemm_w8a8(const int8_t *qa, const float *a_scale, int64_t R, const int32_t *row_index,
+                                       const int32_t *expert_offsets, int32_t E, int64_t K, const int8_t *qw,
+                                       const float *w_scale, int64_t N, int64_t max_slots, float *out,
+                                       hipStream_t stream) {
+    clear_error();
+    W4A8_REQUIRE(expert_offsets && qw && w_scale && (max_slots == 0 || R == 0 || (qa && a_scale && out)), W4A8_EINVAL,
+                 "null pointer");
+    if (w4a8_status st = check_w8(K, N)) return st;
+    W4A8_REQUIRE(R >= 0 && R < (1ll << 31), W4A8_EINVAL, "R=%lld must be in [0, 2^31)", (long long)R);
+    W4A8_REQUIRE(E > 0 && E <= 1024, W4A8_EINVAL, "E=%d must be in [1, 1024]", (int)E);
+    W4A8_REQUIRE(max_slots >= 0 && max_slots < (1ll << 31), W4A8_EINVAL, "bad max_slots");
+    W4A8_REQUIRE(aligned16(qa) && aligned16(qw) && aligned16(out), W4A8_EINVAL,
+                 "qa, qw and out must be 16-byte aligned");
+    if (max_slots == 0 || R == 0) return W4A8_OK;
+    return hip_status(launch_grouped_gemm_w8a8(qa, a_scale, R, row_index, expert_offsets, E, K, qw, w_scale, N,
+                                               max_slots, out, stream),
+                      "grouped_gemm_w8a8 launch");
+}
+
+w4a8_status w4a8_moe_route_scored(const void *logits, int32_t logits_type, int64_t ldl, const float *bias, int64_t T,
+                                  int32_t E, int32_t topk, int32_t with_shared, int32_t score, int32_t n_groups,
+                                  int32_t topk_groups, int32_t group_lead, int32_t renorm, float scale,
+                                  int32_t *topk_ids, float *topk_w, int32_t *expert_offsets, int32_t *perm,
+                                  int32_t *slot_row, int32_t *slot_of_pair, hipStream_t stream) {
+    clear_error();
+    W4A8_REQUIRE(expert_offsets && (T == 0 || (logits && topk_ids && topk_w && perm && slot_of_pair)), W4A8_EINVAL,
+                 "null pointer");
+    W4A8_REQUIRE(T >= 0, W4A8_EINVAL, "T=%lld must be >= 0", (long long)T);
+    W4A8_REQUIRE(E > 0 && E <= kMaxRouteE, W4A8_EINVAL, "E=%d must be in [1, 1024]", (int)E);
+    W4A8_REQUIRE(ldl >= E, W4A8_EINVAL, "ldl=%lld must be at least E=%d", (long long)ldl, (int)E);
+    W4A8_REQUIRE(topk >= 1 && topk <= kMaxRouteK && topk <= E, W4A8_EINVAL, "topk=%d must be in [1, min(E, 32)]",
+                 (int)topk);
+    W4A8_REQUIRE(with_shared == 0 || with_shared == 1, W4A8_EINVAL, "with_shared=%d must be 0 or 1", (int)with_shared);
+    W4A8_REQUIRE(T < (1ll << 31) && T * (topk + 1) < (1ll << 31), W4A8_EINVAL, "T*(topk+1) too large");
+    W4A8_REQUIRE(logits_type == W4A8_F32 || logits_type == W4A8_F16 || logits_type == W4A8_BF16, W4A8_EUNSUPPORTED,
+                 "logits_type=%d is not a supported type", (int)logits_type);
+    W4A8_REQUIRE(((uintptr_t)logits & (logits_type == W4A8_F32 ? 3u : 1u)) == 0, W4A8_EINVAL,
+                 "logits must be aligned to their element");
+    W4A8_REQUIRE(score == W4A8_SCORE_SOFTMAX || score == W4A8_SCORE_SIGMOID, W4A8_EUNSUPPORTED,
+                 "score=%d is not a supported score", (int)score);
+    W4A8_REQUIRE(n_groups >= 1 && n_groups <= kMaxRouteGroups && E % n_groups == 0, W4A8_EINVAL,
+                 "n_groups=%d must be in [1, 64] and divide E=%d", (int)n_groups, (int)E);
+    W4A8_REQUIRE(topk_groups >= 1 && topk_groups <= n_groups, W4A8_EINVAL, "topk_groups=%d must be in [1, n_groups]",
+                 (int)topk_groups);
+    W4A8_REQUIRE(topk <= topk_groups * (E / n_groups), W4A8_EINVAL, "topk=%d exceeds the experts of %d groups",
+                 (int)topk, (int)topk_groups);
+    W4A8_REQUIRE((group_lead == 1 || group_lead == 2) && group_lead <= E / n_groups, W4A8_EINVAL,
+                 "group_lead=%d must be 1 or 2 and at most the group size", (int)group_lead);
+    W4A8_REQUIRE(renorm == 0 || renorm == 1, W4A8_EINVAL, "renorm=%d must be 0 or 1", (int)renorm);
+    W4A8_REQUIRE(std::isfinite(scale), W4A8_EINVAL, "scale must be finite");
+    const RouteCfg cfg{topk, score, n_groups, topk_groups, group_lead, renorm, scale};
+    return hip_status(launch_moe_route_scored(logits, logits_type, ldl, bias, T, E, with_shared, cfg, topk_ids, topk_w,
+                                              expert_offsets, perm, slot_row, slot_of_pair, stream),
+                      "moe_route_scored launch");
 }
 
 w4a8_status w4a8_silu_mul_quantize(const float *gu, int64_t P, int64_t I, int8_t *qh, float *h_scale, float *h_out,
