@@ -7,6 +7,7 @@
 // The same product runs dense, and per expert over the slot lists of the router.  The sums are
 // integers, so neither the order of k nor a split of it changes a result.
 #include <algorithm>
+#include <type_traits>
 
 #include "w8_internal.hpp"
 
@@ -78,6 +79,8 @@ __device__ __forceinline__ void tile_unit(uint8_t *lds, const int8_t *__restrict
     const int full = (int)(K >> 7), steps = (int)((K + 127) >> 7);  // whole stages, all stages
     const int tail = (int)(K & 127) >> 4;                          // chunks of a last part stage
 
+    constexpr int kReads = C::RB + C::CB, kMul = C::RB * C::CB, kLoads = C::LA + C::LB;
+
     // ---- loads: lane L of load j fills chunk L & 7 of row 8 (L? wave + j) + (L >> 3)
     const int8_t *aptr[C::LA];
     uint32_t boff[C::LB];
@@ -98,33 +101,37 @@ __device__ __forceinline__ void tile_unit(uint8_t *lds, const int8_t *__restrict
         bch[j] = (lane & 7) ^ C::key_b(r);
         boff[j] = (uint32_t)(c * K) + 16u * (uint32_t)bch[j];
     }
+    auto load_one = [&](int g, int st, int j) {  // load j of a whole stage
+        if (j < C::LB)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rb, (lds_ptr_t)(lds + st * C::kStage + C::kStageA + 1024 * (C::LB * wave + j)), 16, (int)boff[j % C::LB],
+                g * 128, 0, 0);
+        else
+            __builtin_amdgcn_global_load_lds((glb_ptr_t)(aptr[(j - C::LB) % C::LA] + (int64_t)g * 128),
+                                             (lds_ptr_t)(lds + st * C::kStage + 1024 * (C::LA * wave + j - C::LB)), 16, 0,
+                                             0);
+    };
     auto issue = [&](int g, int st) {
-        uint8_t *da = lds + st * C::kStage + 1024 * (C::LA * wave);
-        uint8_t *db = lds + st * C::kStage + C::kStageA + 1024 * (C::LB * wave);
         if (g < full) {
 #pragma unroll
-            for (int j = 0; j < C::LB; ++j)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(db + 1024 * j), 16, (int)boff[j], g * 128, 0, 0);
-#pragma unroll
-            for (int j = 0; j < C::LA; ++j)
-                __builtin_amdgcn_global_load_lds((glb_ptr_t)(aptr[j] + (int64_t)g * 128), (lds_ptr_t)(da + 1024 * j), 16,
-                                                 0, 0);
+            for (int j = 0; j < kLoads; ++j) load_one(g, st, j);
         } else {
-            // the part stage: chunks past K are zeros on the activations' side (whatever the other
-            // side's buffer holds there) and not loaded
+            // the part stage: chunks past K are not loaded; on the activations' side they are zeros,
+            // so whatever the weights' side of the buffer holds there counts for nothing
 #pragma unroll
             for (int j = 0; j < C::LB; ++j)
-                if (bch[j] < tail)
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(db + 1024 * j), 16, (int)boff[j], g * 128,
-                                                             0, 0);
+                if (bch[j] < tail) load_one(g, st, j);
 #pragma unroll
             for (int j = 0; j < C::LA; ++j) {
-                if (ach[j] < tail)
-                    __builtin_amdgcn_global_load_lds((glb_ptr_t)(aptr[j] + (int64_t)g * 128),
-                                                     (lds_ptr_t)(da + 1024 * j), 16, 0, 0);
-                else *reinterpret_cast<v4i *>(da + 1024 * j + 16 * lane) = v4i{0, 0, 0, 0};
+                if (ach[j] < tail) load_one(g, st, C::LB + j);
+                else
+                    *reinterpret_cast<v4i *>(lds + st * C::kStage + 1024 * (C::LA * wave + j) + 16 * lane) =
+                        v4i{0, 0, 0, 0};
             }
         }
+        // the counted waits need the stages' loads in order
+        __asm__ volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
     };
 
     // ---- fragments: lane l takes row (l & 15) of a block, chunk 4 ks + (l >> 4)
@@ -139,64 +146,82 @@ __device__ __forceinline__ void tile_unit(uint8_t *lds, const int8_t *__restrict
     struct Frags {
         v4i a[C::RB], b[C::CB];
     };
-    auto read = [&](Frags &f, int st, int ks) {
-        const uint8_t *pa = lds + st * C::kStage + aofs[ks], *pb = lds + st * C::kStage + bofs[ks];
-#pragma unroll
-        for (int j = 0; j < C::CB; ++j) f.b[j] = *reinterpret_cast<const v4i *>(pb + 512 * j);  // wrow steps by 4
-#pragma unroll
-        for (int i = 0; i < C::RB; ++i) f.a[i] = *reinterpret_cast<const v4i *>(pa + 2048 * i);
+    auto read_one = [&](Frags &f, int st, int ks, int r) {
+        const uint8_t *base = lds + st * C::kStage;
+        if (r < C::CB) f.b[r % C::CB] = *reinterpret_cast<const v4i *>(base + bofs[ks] + 512 * r);  // wrow steps by 4
+        else f.a[(r - C::CB) % C::RB] = *reinterpret_cast<const v4i *>(base + aofs[ks] + 2048 * (r - C::CB));
     };
     v4i acc[C::RB][C::CB] = {};
-    auto mul = [&](const Frags &f) {
+    // Products of the half in `now`; after each of them one fragment of the half after it (stage st,
+    // half ks, if rd) and after every second one a load of stage g into the buffer sti (if ld), in
+    // just this order: the reads are then back long before the half ends, and no burst of loads
+    // holds up the products.  (The compiler's own order put the reads behind the loads, at the end.)
+    auto half = [&](const Frags &now, auto rd, Frags &then, int st, int ks, auto ld, int g, int sti) {
+        // read r and load d follow these products (a small tile has fewer products than reads or loads)
+        constexpr auto read_at = [](int r) { return kMul > kReads + 2 ? r + 2 : r * kMul / kReads; };
+        constexpr auto load_at = [](int d) { return kMul >= 2 * kLoads ? 2 * d + 1 : d * kMul / kLoads; };
+        int r = 0, d = 0;
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < C::RB; ++i)
-#pragma unroll
-            for (int j = 0; j < C::CB; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
-    };
-    // reads of the next half spread between the products of this one
-    auto interleave = [&]() {
-        constexpr int R = C::RB + C::CB, M = C::RB * C::CB, PER = M / R > 0 ? M / R : 1;
-#pragma unroll
-        for (int q = 0; q < R; ++q) {
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);
+        for (int m = 0; m < kMul; ++m) {
+            const int i = m / C::CB, j = m % C::CB;
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(now.b[j], now.a[i], acc[i][j], 0, 0, 0);
+            if constexpr (decltype(rd)::value)
+                for (; r < kReads && read_at(r) <= m; ++r) read_one(then, st, ks, r);
+            if constexpr (decltype(ld)::value)
+                for (; d < kLoads && load_at(d) <= m; ++d) load_one(g, sti, d);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_group_barrier(0x008, M, 0);
     };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    // a barrier that leaves `vm` loads in flight, with every LDS access done
+    auto stage_barrier = [&](auto vm) {
+        __asm__ volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(waitcnt(decltype(vm)::value, 0));
+        __builtin_amdgcn_s_barrier();
+        __asm__ volatile("" ::: "memory");
+    };
+    using Ahead = std::integral_constant<int, (C::NST - 2) * kLoads>;  // the stages behind the next one
+    using None = std::integral_constant<int, 0>;
 
-    // ---- prologue
+    // ---- prologue: NST stages on their way, stage 0's first half into registers
 #pragma unroll
     for (int g = 0; g < C::NST; ++g)
         if (g < steps) issue(g, g);
-    __builtin_amdgcn_s_waitcnt(waitcnt(0, 0));
-    __builtin_amdgcn_s_barrier();
-    __asm__ volatile("" ::: "memory");
+    if (C::NST <= full) {
+        using First = std::integral_constant<int, (C::NST - 1) * kLoads>;
+        stage_barrier(First{});
+    } else {
+        stage_barrier(None{});
+    }
     Frags f0, f1;
-    read(f0, 0, 0);
-    int st = 0;
-    for (int g = 0; g < steps - 1; ++g) {
-        read(f1, st, 1);
-        mul(f0);
-        interleave();
-        __asm__ volatile("" ::: "memory");
-        // stage g + 1 has landed; the NST - 2 stages behind it may be in flight (a part stage
-        // among them has fewer loads: wait for all)
-        if (C::NST > 2 && g + C::NST - 1 < full)
-            __builtin_amdgcn_s_waitcnt(waitcnt((C::NST - 2) * (C::LA + C::LB), 0));
-        else __builtin_amdgcn_s_waitcnt(waitcnt(0, 0));
-        __builtin_amdgcn_s_barrier();
-        __asm__ volatile("" ::: "memory");
+#pragma unroll
+    for (int r = 0; r < kReads; ++r) read_one(f0, 0, 0, r);
+    int st = 0, g = 0;
+    auto lds_wait = [&]() {  // f0 is back (or nearly) before new reads are issued behind it
+        __builtin_amdgcn_s_waitcnt(waitcnt(63, 0));
+    };
+    for (; g + C::NST < full; ++g) {
+        lds_wait();
+        half(f0, Yes{}, f1, st, 1, No{}, 0, 0);
+        stage_barrier(Ahead{});
+        const int sti = st;
+        st = st + 1 == C::NST ? 0 : st + 1;
+        half(f1, Yes{}, f0, st, 0, Yes{}, g + C::NST, sti);
+    }
+    // the last stages: fewer loads in flight, or a part stage's: every wait is for all of them
+    for (; g < steps - 1; ++g) {
+        lds_wait();
+        half(f0, Yes{}, f1, st, 1, No{}, 0, 0);
+        stage_barrier(None{});
         if (g + C::NST < steps) issue(g + C::NST, st);
         st = st + 1 == C::NST ? 0 : st + 1;
-        read(f0, st, 0);
-        mul(f1);
-        interleave();
+        half(f1, Yes{}, f0, st, 0, No{}, 0, 0);
     }
-    read(f1, st, 1);
-    mul(f0);
-    interleave();
-    mul(f1);
+    lds_wait();
+    half(f0, Yes{}, f1, st, 1, No{}, 0, 0);
+    half(f1, No{}, f0, st, 0, No{}, 0, 0);
 
     // ---- epilogue: lane l holds row 16 i + (l & 15) and, of block j, channels 4 CB (l >> 4) + 4 j + r
     const int64_t nb = n0 + wn * C::CB * 16 + 4 * C::CB * qd;
@@ -270,100 +295,260 @@ __global__ __launch_bounds__(C::kThreads) void gemm_w8a8_tile_kernel(const int8_
                     ldo, vec);
 }
 
-using Tile256 = Tile<256, 256, 2, 4, 2>;
-using Tile128 = Tile<128, 128, 2, 2, 2>;
+// ------------------------------------------------------------------ few rows
+// Up to 16 MT rows: the weights are the whole cost.  A workgroup of SPLIT waves takes 16 output
+// channels; its waves take turns at the 128-byte windows of k, each with a ring of U windows in
+// registers, and their int32 sums meet in LDS once at the end.
+// A load instruction covers whole 128-byte lines: lane L of load j reads channel 8 j + (L & 7),
+// chunk L >> 3 of the window.  The product wants lane l to hold channel l & 15 and, in its two
+// steps, the chunks 2 (l >> 4) and 2 (l >> 4) + 1: for channels 0-7 the one is the lane's own and
+// the other lane l + 8's, for channels 8-15 the other way round -- a rotation by 8 of each 16
+// lanes, written to half of them.  Activation rows come from the caches.
+template <int BANKS>
+__device__ __forceinline__ v4i ror8_into(v4i old, v4i src) {
+    v4i r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __builtin_amdgcn_update_dpp(old[i], src[i], 0x128, 0xF, BANKS, false);
+    return r;
+}
 
-// ------------------------------------------------------------------ plain tile
-// A 256-thread workgroup computes a 64 x 64 tile, four waves of 32 x 32 on
-// v_mfma_i32_16x16x64_i8; 64 bytes of k are staged per step through registers into LDS rows
-// padded to 80 bytes.  Rows and columns outside, and k past K, are staged as zeros.
-constexpr int kTileThreads = 256, kTile = 64, kStepK = 64, kRow = 80;
+template <int MT, int SPLIT, int U, typename T, typename SrcRow>
+__device__ __forceinline__ void stream_unit(v4i (*red)[MT][64], const int8_t *__restrict__ qa,
+                                            const float *__restrict__ a_scale, SrcRow src_row, int64_t slot0, int rows,
+                                            int64_t K, const int8_t *__restrict__ qw,
+                                            const float *__restrict__ w_scale, int64_t N, int64_t n0,
+                                            const float *__restrict__ bias, T *__restrict__ out, int64_t ldo, bool vec) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int qd = lane >> 4;
+    const int full = (int)(K >> 7), tail = (int)(K & 127) >> 4;  // whole windows, chunks of a part window
+    const int mine = full > wave ? (full - wave + SPLIT - 1) / SPLIT : 0;
 
-template <typename T, typename SrcRow>
-__device__ __forceinline__ void plain_unit(uint8_t *lds, const int8_t *__restrict__ qa,
-                                          const float *__restrict__ a_scale, SrcRow src_row, int64_t slot0, int rows,
-                                          int64_t K, const int8_t *__restrict__ qw,
-                                          const float *__restrict__ w_scale, int64_t N, int64_t n0,
-                                          const float *__restrict__ bias, T *__restrict__ out, int64_t ldo) {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wm = wave >> 1, wn = wave & 1;
-    const int lr = tid >> 2, lc = (tid & 3) * 16;
-    const int64_t arow = lr < rows ? src_row(lr) : -1;
-    const int64_t col = n0 + lr;
-    v4i acc[2][2] = {};
-    for (int64_t k0 = 0; k0 < K; k0 += kStepK) {
-        const bool kin = k0 + lc < K;
-        v4i a = {}, b = {};
-        if (kin && arow >= 0) a = *reinterpret_cast<const v4i *>(qa + arow * K + k0 + lc);
-        if (kin && col < N) b = *reinterpret_cast<const v4i *>(qw + col * K + k0 + lc);
-        __syncthreads();
-        *reinterpret_cast<v4i *>(lds + lr * kRow + lc) = a;
-        *reinterpret_cast<v4i *>(lds + (kTile + lr) * kRow + lc) = b;
-        __syncthreads();
-        v4i af[2], bf[2];
+    const int8_t *wp[2], *ap[MT];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            af[i] = *reinterpret_cast<const v4i *>(lds + (wm * 32 + i * 16 + (lane & 15)) * kRow + (lane >> 4) * 16);
-            bf[i] = *reinterpret_cast<const v4i *>(lds + (kTile + wn * 32 + i * 16 + (lane & 15)) * kRow +
-                                                   (lane >> 4) * 16);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[i], bf[j], acc[i][j], 0, 0, 0);
+    for (int j = 0; j < 2; ++j) {
+        const int64_t c = n0 + 8 * j + (lane & 7);
+        wp[j] = qw + (c < N ? c : N - 1) * K;
     }
-    // accumulator: rows 4 (l >> 4) + r, column l & 15
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int t = 0; t < MT; ++t) {
+        const int r = 16 * t + (lane & 15);
+        const int64_t src = src_row(r < rows ? r : rows - 1);
+        ap[t] = qa + (src < 0 ? 0 : src) * K;
+    }
+    struct Window {
+        v4i w[2], a[MT][2];
+    };
+    auto load = [&](Window &x, int i) {  // window i, all of it
+        const int64_t k = (int64_t)i * 128;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int m = wm * 32 + i * 16 + 4 * (lane >> 4) + r;
-            const int64_t row = m < rows ? src_row(m) : -1;
-            if (row < 0) continue;
-            const float as = a_scale[row];
+        for (int j = 0; j < 2; ++j)
+            x.w[j] = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(wp[j] + k + 16 * (lane >> 3)));
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int64_t n = n0 + wn * 32 + j * 16 + (lane & 15);
-                if (n < N)
-                    out[(slot0 + m) * ldo + n] =
-                        finish<T>(acc[i][j][r], as, w_scale[n], bias ? bias[n] : 0.0f, bias != nullptr);
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) x.a[t][s] = *reinterpret_cast<const v4i *>(ap[t] + k + 32 * qd + 16 * s);
+    };
+    v4i acc[MT] = {};
+    auto mul = [&](const Window &x) {
+        const v4i w0 = ror8_into<0xC>(x.w[0], x.w[1]), w1 = ror8_into<0x3>(x.w[1], x.w[0]);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w0, x.a[t][0], acc[t], 0, 0, 0);
+            acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w1, x.a[t][1], acc[t], 0, 0, 0);
+        }
+    };
+    if (mine > 0) {
+        Window ring[U];
+        // past the last window it is loaded again, so that every wait counts the same loads
+        auto at = [&](int i) { return wave + SPLIT * (i < mine ? i : mine - 1); };
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            __builtin_amdgcn_sched_barrier(0);
+            load(ring[u], at(u));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        for (int i0 = 0; i0 < mine; i0 += U) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (i0 + u < mine) mul(ring[u]);
+                __builtin_amdgcn_sched_barrier(0);
+                load(ring[u], at(i0 + u + U));
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
+    }
+    if (tail && wave == full % SPLIT) {  // chunks past K: any weights against zeros
+        Window x;
+        const int64_t k = (int64_t)full * 128;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int c = lane >> 3;
+            x.w[j] = *reinterpret_cast<const v4i *>(wp[j] + k + 16 * (c < tail ? c : 0));
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int c = 2 * qd + s;
+                x.a[t][s] = *reinterpret_cast<const v4i *>(ap[t] + k + 16 * (c < tail ? c : 0));
+                if (c >= tail) x.a[t][s] = v4i{0, 0, 0, 0};
+            }
+        mul(x);
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t) red[wave][t][lane] = acc[t];
+    __syncthreads();
+    // lane l of the wave that ends tile t holds row 16 t + (l & 15), channels 4 (l >> 4) + r
+    for (int t = wave; t < MT; t += SPLIT) {
+        v4i s = red[0][t][lane];
+#pragma unroll
+        for (int w = 1; w < SPLIT; ++w) s += red[w][t][lane];
+        const int m = 16 * t + (lane & 15);
+        const int64_t row = m < rows ? src_row(m) : -1;
+        if (row < 0) continue;
+        const float as = a_scale[row];
+        const int64_t nb = n0 + 4 * qd;
+        T *o = out + (slot0 + m) * ldo + nb;
+        typedef T vt __attribute__((ext_vector_type(4)));
+        vt v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int64_t n = nb + r < N ? nb + r : N - 1;
+            v[r] = finish<T>(s[r], as, w_scale[n], bias ? bias[n] : 0.0f, bias != nullptr);
+        }
+        if (vec && nb + 4 <= N) *reinterpret_cast<vt *>(o) = v;
+        else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (nb + r < N) o[r] = v[r];
+        }
+    }
+}
+
+template <int MT, int SPLIT, int U, typename T>
+__global__ __launch_bounds__(64 * SPLIT) void gemm_w8a8_stream_kernel(const int8_t *__restrict__ qa,
+                                                                      const float *__restrict__ a_scale, int64_t M,
+                                                                      int64_t K, const int8_t *__restrict__ qw,
+                                                                      const float *__restrict__ w_scale, int64_t N,
+                                                                      const float *__restrict__ bias,
+                                                                      T *__restrict__ out, int64_t ldo, bool vec) {
+    __shared__ v4i red[SPLIT][MT][64];
+    stream_unit<MT, SPLIT, U, T>(red, qa, a_scale, [](int r) { return (int64_t)r; }, 0, (int)M, K, qw, w_scale, N,
+                                 (int64_t)blockIdx.x * 16, bias, out, ldo, vec);
+}
+
+// ------------------------------------------------------------------ per expert
+constexpr int kMaxE = 1024;
+
+// Activation row of a unit's row r: row_index of its slot (or the slot), -1 outside [0, R).
+struct SlotRows {
+    const int32_t *row_index;
+    int64_t slot0, R;
+    __device__ int64_t operator()(int r) const {
+        const int64_t row = row_index ? (int64_t)row_index[slot0 + r] : slot0 + r;
+        return row >= 0 && row < R ? row : -1;
+    }
+};
+
+// Work units of the experts with lo < slots <= hi: ceil(slots / bm) row blocks each, times nt column
+// tiles.  pfx[0 .. E] receives the exclusive prefix of the row blocks over experts (whole
+// workgroup; E <= 1024).
+__device__ __forceinline__ void block_prefix(int32_t *pfx, const int32_t *__restrict__ offsets, int32_t E,
+                                             int64_t max_slots, int lo, int hi, int bm) {
+    __shared__ int32_t part[16];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nw = blockDim.x >> 6;
+    const int per = (E + blockDim.x - 1) / blockDim.x;  // <= 16 experts per thread
+    auto blocks = [&](int e) -> int32_t {
+        const int64_t c = clamp_slots(offsets[e + 1], max_slots) - clamp_slots(offsets[e], max_slots);
+        return c > lo && c <= hi ? (int32_t)((c + bm - 1) / bm) : 0;
+    };
+    const int e0 = tid * per, e1 = e0 + per < E ? e0 + per : E;
+    int32_t own = 0;
+    for (int e = e0; e < e1; ++e) own += blocks(e);
+    int32_t incl = own;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int32_t o = __shfl_up(incl, off, 64);
+        if (lane >= off) incl += o;
+    }
+    if (lane == 63) part[wave] = incl;
+    __syncthreads();
+    int32_t run = incl - own;
+    for (int w = 0; w < wave; ++w) run += part[w];
+    for (int e = e0; e < e1; ++e) {
+        pfx[e] = run;
+        run += blocks(e);
+    }
+    if (tid == 0) {
+        int32_t total = 0;
+        for (int w = 0; w < nw; ++w) total += part[w];
+        pfx[E] = total;
+    }
     __syncthreads();
 }
 
-template <typename T>
-__global__ __launch_bounds__(kTileThreads) void gemm_w8a8_plain_kernel(const int8_t *__restrict__ qa,
-                                                                 const float *__restrict__ a_scale, int64_t M,
-                                                                 int64_t K, const int8_t *__restrict__ qw,
-                                                                 const float *__restrict__ w_scale, int64_t N,
-                                                                 const float *__restrict__ bias, T *__restrict__ out,
-                                                                 int64_t ldo) {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kTile * kRow];
-    const int64_t nt = (N + kTile - 1) / kTile;
-    const int64_t m0 = (int64_t)blockIdx.x / nt * kTile, n0 = (int64_t)blockIdx.x % nt * kTile;
-    const int rows = (int)((M - m0) < kTile ? (M - m0) : kTile);
-    plain_unit<T>(lds, qa, a_scale, [&](int r) { return m0 + r; }, m0, rows, K, qw, w_scale, N, n0, bias, out, ldo);
+// the expert of row block u: the last e with pfx[e] <= u
+__device__ __forceinline__ int find_expert(const int32_t *pfx, int32_t E, int32_t u) {
+    int lo = 0, hi = E;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pfx[mid] <= u) lo = mid;
+        else hi = mid;
+    }
+    return lo;
 }
 
-// One workgroup per (64-column tile, expert), walking the expert's slots 64 at a time.
-__global__ __launch_bounds__(kTileThreads) void grouped_w8a8_kernel(
+// Experts of up to 16 slots, a persistent grid over their 16-channel tiles.
+template <int SPLIT, int U>
+__global__ __launch_bounds__(64 * SPLIT) void grouped_w8a8_stream_kernel(
     const int8_t *__restrict__ qa, const float *__restrict__ a_scale, int64_t R, const int32_t *__restrict__ row_index,
-    const int32_t *__restrict__ offsets, int64_t K, const int8_t *__restrict__ qw, const float *__restrict__ w_scale,
-    int64_t N, int64_t max_slots, float *__restrict__ out) {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kTile * kRow];
-    const int64_t e = blockIdx.y, n0 = (int64_t)blockIdx.x * kTile;
-    const int64_t s0 = clamp_slots(offsets[e], max_slots), s1 = clamp_slots(offsets[e + 1], max_slots);
-    for (int64_t s = s0; s < s1; s += kTile) {
-        const int rows = (int)((s1 - s) < kTile ? (s1 - s) : kTile);
-        auto src = [&](int r) -> int64_t {
-            const int64_t row = row_index ? (int64_t)row_index[s + r] : s + r;
-            return row >= 0 && row < R ? row : -1;
-        };
-        plain_unit<float>(lds, qa, a_scale, src, s, rows, K, qw + e * N * K, w_scale + e * N, N, n0, nullptr, out, N);
+    const int32_t *__restrict__ offsets, int32_t E, int64_t K, const int8_t *__restrict__ qw,
+    const float *__restrict__ w_scale, int64_t N, int64_t max_slots, int hi, float *__restrict__ out) {
+    __shared__ v4i red[SPLIT][1][64];
+    __shared__ int32_t pfx[kMaxE + 1];
+    block_prefix(pfx, offsets, E, max_slots, 0, hi, 16);
+    const int64_t nt = (N + 15) / 16, units = pfx[E] * nt;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int32_t b = (int32_t)(u / nt);
+        const int64_t e = find_expert(pfx, E, b);
+        const int64_t s0 = clamp_slots(offsets[e], max_slots) + 16 * (b - pfx[e]);
+        const int64_t left = clamp_slots(offsets[e + 1], max_slots) - s0;
+        stream_unit<1, SPLIT, U, float>(red, qa, a_scale, SlotRows{row_index, s0, R}, s0, left < 16 ? (int)left : 16, K,
+                                        qw + e * N * K, w_scale + e * N, N, u % nt * 16, nullptr, out, N, N % 4 == 0);
+        __syncthreads();  // red is taken again by the next unit
     }
 }
+
+// Experts with lo < slots <= hi on C's tiles: a persistent grid over (row block, column tile)
+// units, an expert's row blocks next to each other on one XCD, so that its weights come
+// through one L2.
+template <typename C>
+__global__ __launch_bounds__(C::kThreads) void grouped_w8a8_tile_kernel(
+    const int8_t *__restrict__ qa, const float *__restrict__ a_scale, int64_t R, const int32_t *__restrict__ row_index,
+    const int32_t *__restrict__ offsets, int32_t E, int64_t K, const int8_t *__restrict__ qw,
+    const float *__restrict__ w_scale, int64_t N, int64_t max_slots, int lo, int hi, float *__restrict__ out) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kLds];
+    __shared__ int32_t pfx[kMaxE + 1];
+    block_prefix(pfx, offsets, E, max_slots, lo, hi, C::BM);
+    const int64_t nt = (N + C::BN - 1) / C::BN, units = pfx[E] * nt;
+    const int64_t per = gridDim.x / 8;  // the grid is a multiple of 8
+    for (int64_t u = blockIdx.x % 8 * per + blockIdx.x / 8; u < units; u += gridDim.x) {
+        // unit order: expert, column tile, row block
+        const int e = find_expert(pfx, E, (int32_t)(u / nt));
+        const int64_t first = pfx[e] * nt, nb = pfx[e + 1] - pfx[e];
+        const int64_t b = (u - first) % nb, tn = (u - first) / nb;
+        const int64_t s0 = clamp_slots(offsets[e], max_slots) + C::BM * b;
+        const int64_t left = clamp_slots(offsets[e + 1], max_slots) - s0;
+        tile_unit<C, float>(lds, qa, a_scale, SlotRows{row_index, s0, R}, s0, left < C::BM ? (int)left : C::BM, K,
+                            qw + e * N * K, w_scale + e * N, N, tn * C::BN, nullptr, out, N, N % 4 == 0);
+        __syncthreads();  // the LDS stages are taken again by the next unit
+    }
+}
+
+using Tile256 = Tile<256, 256, 2, 4, 2>;
+using Tile128 = Tile<128, 256, 2, 4, 3>;
+using Tile64 = Tile<64, 256, 2, 4, 3>;
+constexpr int kCus = 256;
 
 }  // namespace
 
@@ -374,8 +559,17 @@ static hipError_t launch_tile(const int8_t *qa, const float *a_scale, int64_t M,
                               const float *w_scale, int64_t N, const float *bias, T *out, int64_t ldo, bool vec,
                               hipStream_t stream) {
     const int64_t tiles = ((M + C::BM - 1) / C::BM) * ((N + C::BN - 1) / C::BN);
-    hipLaunchKernelGGL((gemm_w8a8_tile_kernel<C, T>), dim3((uint32_t)tiles), dim3(C::kThreads), 0, stream, qa,
-                       a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec);
+    hipLaunchKernelGGL((gemm_w8a8_tile_kernel<C, T>), dim3((uint32_t)tiles), dim3(C::kThreads), 0, stream, qa, a_scale,
+                       M, K, qw, w_scale, N, bias, out, ldo, vec);
+    return hipGetLastError();
+}
+
+template <int MT, int SPLIT, int U, typename T>
+static hipError_t launch_stream(const int8_t *qa, const float *a_scale, int64_t M, int64_t K, const int8_t *qw,
+                                const float *w_scale, int64_t N, const float *bias, T *out, int64_t ldo, bool vec,
+                                hipStream_t stream) {
+    hipLaunchKernelGGL((gemm_w8a8_stream_kernel<MT, SPLIT, U, T>), dim3((uint32_t)((N + 15) / 16)), dim3(64 * SPLIT), 0,
+                       stream, qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec);
     return hipGetLastError();
 }
 
@@ -384,8 +578,11 @@ static hipError_t gemm_w8a8_typed(const int8_t *qa, const float *a_scale, int64_
                                   const float *w_scale, int64_t N, const float *bias, T *out, int64_t ldo,
                                   hipStream_t stream) {
     const bool vec = (uintptr_t)out % 16 == 0 && ldo * (int64_t)sizeof(T) % 16 == 0;
-    if (M > 128) return launch_tile<Tile256>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream);
-    return launch_tile<Tile128>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream);
+    if (M <= 16) return launch_stream<1, 8, 4>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream);
+    if (M <= 32) return launch_stream<2, 8, 4>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream);
+    if (M <= 64) return launch_tile<Tile64>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream);
+    if (M <= 128) return launch_tile<Tile128>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream);
+    return launch_tile<Tile256>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream);
 }
 
 hipError_t launch_gemm_w8a8(const int8_t *qa, const float *a_scale, int64_t M, int64_t K, const int8_t *qw,
@@ -401,14 +598,37 @@ hipError_t launch_gemm_w8a8(const int8_t *qa, const float *a_scale, int64_t M, i
     }
 }
 
+template <typename C>
+static hipError_t launch_grouped_tile(const int8_t *qa, const float *a_scale, int64_t R, const int32_t *row_index,
+                                      const int32_t *offsets, int32_t E, int64_t K, const int8_t *qw,
+                                      const float *w_scale, int64_t N, int64_t max_slots, int lo, int hi, float *out,
+                                      hipStream_t stream) {
+    // the most units there can be: every expert of the class has more than lo slots
+    const int64_t blocks = std::min<int64_t>((int64_t)E, max_slots / (lo + 1)) + max_slots / C::BM;
+    const int64_t units = blocks * ((N + C::BN - 1) / C::BN);
+    const int64_t grid = std::min<int64_t>((units + 7) / 8 * 8, kCus);
+    hipLaunchKernelGGL((grouped_w8a8_tile_kernel<C>), dim3((uint32_t)grid), dim3(C::kThreads), 0, stream, qa, a_scale, R,
+                       row_index, offsets, E, K, qw, w_scale, N, max_slots, lo, hi, out);
+    return hipGetLastError();
+}
+
 hipError_t launch_grouped_gemm_w8a8(const int8_t *qa, const float *a_scale, int64_t R, const int32_t *row_index,
                                     const int32_t *expert_offsets, int32_t E, int64_t K, const int8_t *qw,
                                     const float *w_scale, int64_t N, int64_t max_slots, float *out,
                                     hipStream_t stream) {
-    const dim3 grid((uint32_t)((N + kTile - 1) / kTile), (uint32_t)E);
-    hipLaunchKernelGGL(grouped_w8a8_kernel, grid, dim3(kTileThreads), 0, stream, qa, a_scale, R, row_index,
-                       expert_offsets, K, qw, w_scale, N, max_slots, out);
-    return hipGetLastError();
+    constexpr int SPLIT = 8, kStreamMax = 16, kTile64Max = 64;
+    const int64_t units = std::min<int64_t>(E, max_slots) * ((N + 15) / 16);
+    const int64_t grid = std::min<int64_t>(units, kCus * 4);
+    hipLaunchKernelGGL((grouped_w8a8_stream_kernel<SPLIT, 4>), dim3((uint32_t)grid), dim3(64 * SPLIT), 0, stream, qa,
+                       a_scale, R, row_index, expert_offsets, E, K, qw, w_scale, N, max_slots, kStreamMax, out);
+    hipError_t err = hipGetLastError();
+    if (err == hipSuccess && max_slots > kStreamMax)
+        err = launch_grouped_tile<Tile64>(qa, a_scale, R, row_index, expert_offsets, E, K, qw, w_scale, N, max_slots,
+                                          kStreamMax, kTile64Max, out, stream);
+    if (err == hipSuccess && max_slots > kTile64Max)
+        err = launch_grouped_tile<Tile128>(qa, a_scale, R, row_index, expert_offsets, E, K, qw, w_scale, N, max_slots,
+                                           kTile64Max, 0x7FFFFFFF, out, stream);
+    return err;
 }
 
 }  // namespace w4a8
