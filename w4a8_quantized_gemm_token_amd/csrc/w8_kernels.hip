@@ -51,6 +51,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *p) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)0xFFFFFFFF, 0x00020000);
 }
 
+// A value that every lane holds alike, for the scalar registers (a resource descriptor that the
+// compiler cannot prove uniform costs a loop over its values at every load).
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+    return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
 template <int BM_, int BN_, int WM_, int WN_, int NST_>
 struct Tile {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_;
@@ -93,7 +100,7 @@ __device__ __forceinline__ void tile_unit(uint8_t *lds, const int8_t *__restrict
         ach[j] = (lane & 7) ^ C::key_a(r);
         aptr[j] = qa + src * K + 16 * ach[j];
     }
-    const __amdgpu_buffer_rsrc_t rb = make_rsrc(qw + n0 * K);
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc((const void *)uniform((int64_t)(qw + n0 * K)));
 #pragma unroll
     for (int j = 0; j < C::LB; ++j) {
         const int r = 8 * (C::LB * wave + j) + (lane >> 3);
@@ -452,10 +459,11 @@ struct SlotRows {
 
 // Work units of the experts with lo < slots <= hi: ceil(slots / bm) row blocks each, times nt column
 // tiles.  pfx[0 .. E] receives the exclusive prefix of the row blocks over experts (whole
-// workgroup; E <= 1024).
+// workgroup; E <= 1024); pfx[kMaxE + 1 ..] is scratch.
+constexpr int kPfx = kMaxE + 1 + 16;
 __device__ __forceinline__ void block_prefix(int32_t *pfx, const int32_t *__restrict__ offsets, int32_t E,
                                              int64_t max_slots, int lo, int hi, int bm) {
-    __shared__ int32_t part[16];
+    int32_t *part = pfx + kMaxE + 1;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nw = blockDim.x >> 6;
     const int per = (E + blockDim.x - 1) / blockDim.x;  // <= 16 experts per thread
     auto blocks = [&](int e) -> int32_t {
@@ -495,7 +503,7 @@ __device__ __forceinline__ int find_expert(const int32_t *pfx, int32_t E, int32_
         if (pfx[mid] <= u) lo = mid;
         else hi = mid;
     }
-    return lo;
+    return __builtin_amdgcn_readfirstlane(lo);  // u is the same for the whole workgroup
 }
 
 // Experts of up to 16 slots, a persistent grid over their 16-channel tiles.
@@ -505,7 +513,7 @@ __global__ __launch_bounds__(64 * SPLIT) void grouped_w8a8_stream_kernel(
     const int32_t *__restrict__ offsets, int32_t E, int64_t K, const int8_t *__restrict__ qw,
     const float *__restrict__ w_scale, int64_t N, int64_t max_slots, int hi, float *__restrict__ out) {
     __shared__ v4i red[SPLIT][1][64];
-    __shared__ int32_t pfx[kMaxE + 1];
+    __shared__ int32_t pfx[kPfx];
     block_prefix(pfx, offsets, E, max_slots, 0, hi, 16);
     const int64_t nt = (N + 15) / 16, units = pfx[E] * nt;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
@@ -527,16 +535,18 @@ __global__ __launch_bounds__(C::kThreads) void grouped_w8a8_tile_kernel(
     const int8_t *__restrict__ qa, const float *__restrict__ a_scale, int64_t R, const int32_t *__restrict__ row_index,
     const int32_t *__restrict__ offsets, int32_t E, int64_t K, const int8_t *__restrict__ qw,
     const float *__restrict__ w_scale, int64_t N, int64_t max_slots, int lo, int hi, float *__restrict__ out) {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kLds];
-    __shared__ int32_t pfx[kMaxE + 1];
+    // one LDS object: with several, the compiler tells the loads into LDS and the reads apart by
+    // object and puts a wait for every load in flight before the reads of the stages
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kLds + kPfx * 4];
+    int32_t *pfx = reinterpret_cast<int32_t *>(lds + C::kLds);
     block_prefix(pfx, offsets, E, max_slots, lo, hi, C::BM);
     const int64_t nt = (N + C::BN - 1) / C::BN, units = pfx[E] * nt;
     const int64_t per = gridDim.x / 8;  // the grid is a multiple of 8
     for (int64_t u = blockIdx.x % 8 * per + blockIdx.x / 8; u < units; u += gridDim.x) {
         // unit order: expert, column tile, row block
         const int e = find_expert(pfx, E, (int32_t)(u / nt));
-        const int64_t first = pfx[e] * nt, nb = pfx[e + 1] - pfx[e];
-        const int64_t b = (u - first) % nb, tn = (u - first) / nb;
+        const int64_t p0 = pfx[e], nb = pfx[e + 1] - p0;
+        const int64_t b = (u - p0 * nt) % nb, tn = (u - p0 * nt) / nb;
         const int64_t s0 = clamp_slots(offsets[e], max_slots) + C::BM * b;
         const int64_t left = clamp_slots(offsets[e + 1], max_slots) - s0;
         tile_unit<C, float>(lds, qa, a_scale, SlotRows{row_index, s0, R}, s0, left < C::BM ? (int)left : C::BM, K,
