@@ -303,14 +303,19 @@ __global__ __launch_bounds__(C::kThreads) void gemm_w8a8_tile_kernel(const int8_
 }
 
 // ------------------------------------------------------------------ few rows
-// Up to 16 MT rows: the weights are the whole cost.  A workgroup of SPLIT waves takes 16 output
-// channels; its waves take turns at the 128-byte windows of k, each with a ring of U windows in
-// registers, and their int32 sums meet in LDS once at the end.
+// Up to 16 MT rows: the weights are the whole cost, and each byte of them is used once.  A
+// workgroup's waves share out k in 128-byte windows (wave w has the windows w + W i, i < NW, of
+// a pass of W NW windows; one pass where K allows) and walk the same run of 16-channel tiles, so
+// a wave keeps its slice of the activations in registers for the whole run and does nothing but
+// stream weights through a ring of registers (D tiles deep).  The waves' int32 partial sums of a
+// tile meet in LDS, and one wave after the other ends a tile.
 // A load instruction covers whole 128-byte lines: lane L of load j reads channel 8 j + (L & 7),
 // chunk L >> 3 of the window.  The product wants lane l to hold channel l & 15 and, in its two
 // steps, the chunks 2 (l >> 4) and 2 (l >> 4) + 1: for channels 0-7 the one is the lane's own and
 // the other lane l + 8's, for channels 8-15 the other way round -- a rotation by 8 of each 16
-// lanes, written to half of them.  Activation rows come from the caches.
+// lanes, written to half of them.
+// Channels past N and bytes past the array read as 0 (the descriptor ends with the array); k past
+// K and the windows that a wave has no share of are zeros on the activations' side.
 template <int BANKS>
 __device__ __forceinline__ v4i ror8_into(v4i old, v4i src) {
     v4i r;
@@ -319,129 +324,184 @@ __device__ __forceinline__ v4i ror8_into(v4i old, v4i src) {
     return r;
 }
 
-template <int MT, int SPLIT, int U, typename T, typename SrcRow>
-__device__ __forceinline__ void stream_unit(v4i (*red)[MT][64], const int8_t *__restrict__ qa,
-                                            const float *__restrict__ a_scale, SrcRow src_row, int64_t slot0, int rows,
-                                            int64_t K, const int8_t *__restrict__ qw,
-                                            const float *__restrict__ w_scale, int64_t N, int64_t n0,
-                                            const float *__restrict__ bias, T *__restrict__ out, int64_t ldo, bool vec) {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int qd = lane >> 4;
-    const int full = (int)(K >> 7), tail = (int)(K & 127) >> 4;  // whole windows, chunks of a part window
-    const int mine = full > wave ? (full - wave + SPLIT - 1) / SPLIT : 0;
+constexpr int kMaxSliceWaves = 16;
 
-    const int8_t *wp[2], *ap[MT];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int64_t c = n0 + 8 * j + (lane & 7);
-        wp[j] = qw + (c < N ? c : N - 1) * K;
-    }
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        const int r = 16 * t + (lane & 15);
-        const int64_t src = src_row(r < rows ? r : rows - 1);
-        ap[t] = qa + (src < 0 ? 0 : src) * K;
-    }
-    struct Window {
-        v4i w[2], a[MT][2];
-    };
-    auto load = [&](Window &x, int i) {  // window i, all of it
-        const int64_t k = (int64_t)i * 128;
+// Walk: the tiles of a workgroup's run, one after the other: w and bytes (the weights of the
+// tile's first channel, and from there to the end of the array's or the expert's last row), n0
+// (the first channel), block (the rows stay in registers while it stays), next(), and rows(f),
+// which calls f(src_row, slot0, rows, w_scale).  ONE: a single pass.
+template <int MT, int NW, bool ONE, typename T, typename Walk>
+__device__ __forceinline__ void slice_walk(v4i (*red)[kMaxSliceWaves][MT][64], Walk to_load, int64_t tiles,
+                                           const int8_t *__restrict__ qa, const float *__restrict__ a_scale, int64_t K,
+                                           int passes, int64_t N, const float *__restrict__ bias, T *__restrict__ out,
+                                           int64_t ldo, bool vec) {
+    constexpr int D = 4 / NW > 0 ? 4 / NW : 1;  // tiles in the ring: about 4 windows, 8 KB a wave
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int W = blockDim.x >> 6;
+    const int qd = lane >> 4;
+    const int windows = (int)((K + 127) >> 7);
+    const uint32_t lofs = (uint32_t)(lane & 7) * (uint32_t)K + 16u * (uint32_t)(lane >> 3), row8 = 8u * (uint32_t)K;
+    Walk now = to_load;  // the tile of the products; to_load is D steps ahead
+
+    v4i a[NW][MT][2], ring[D][NW][2];
+    int64_t loaded = 0;
+    int load_pass = 0;
+    auto load = [&](v4i (&x)[NW][2], int i) {  // window i of the next tile (or pass) to load
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            (void *)to_load.w, (short)0, (int)(uint32_t)(to_load.bytes < 0xFFFFFFFFll ? to_load.bytes : 0xFFFFFFFFll),
+            0x00020000);
+        int w = (load_pass * NW + i) * W + wave;
+        w = w < windows ? w : wave < windows ? wave : 0;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            x.w[j] = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(wp[j] + k + 16 * (lane >> 3)));
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) x.a[t][s] = *reinterpret_cast<const v4i *>(ap[t] + k + 32 * qd + 16 * s);
+            x[i][j] = __builtin_bit_cast(
+                v4i, __builtin_amdgcn_raw_buffer_load_b128(rs, lofs + (uint32_t)w * 128u + j * row8, 0, 2));
+        // past the run's end its last tile is loaded again: the waits always count the same loads
+        if (i < NW - 1) return;
+        if (!ONE && ++load_pass < passes) return;
+        load_pass = 0;
+        if (++loaded < tiles) to_load.next();
     };
-    v4i acc[MT] = {};
-    auto mul = [&](const Window &x) {
-        const v4i w0 = ror8_into<0xC>(x.w[0], x.w[1]), w1 = ror8_into<0x3>(x.w[1], x.w[0]);
+    float as[MT];
+    auto load_rows = [&](int pass) {
+        now.rows([&](auto src_row, int64_t, int rows, const float *) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w0, x.a[t][0], acc[t], 0, 0, 0);
-            acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w1, x.a[t][1], acc[t], 0, 0, 0);
-        }
+            for (int t = 0; t < MT; ++t) {
+                const int r = 16 * t + (lane & 15);
+                int64_t src = src_row(r < rows ? r : rows - 1);
+                src = src < 0 ? 0 : src;
+                as[t] = a_scale[src];
+                const int8_t *p = qa + src * K;
+#pragma unroll
+                for (int i = 0; i < NW; ++i) {
+                    const int w = (pass * NW + i) * W + wave;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const int64_t k = (int64_t)w * 128 + 32 * qd + 16 * s;
+                        const v4i v = *reinterpret_cast<const v4i *>(p + (k < K ? k : 0));
+                        a[i][t][s] = k < K ? v : v4i{0, 0, 0, 0};
+                    }
+                }
+            }
+        });
     };
-    if (mine > 0) {
-        Window ring[U];
-        // past the last window it is loaded again, so that every wait counts the same loads
-        auto at = [&](int i) { return wave + SPLIT * (i < mine ? i : mine - 1); };
+    int64_t block = now.block;
+    if (ONE) load_rows(0);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+    for (int d = 0; d < D; ++d)
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
             __builtin_amdgcn_sched_barrier(0);
-            load(ring[u], at(u));
+            load(ring[d], i);
         }
-        __builtin_amdgcn_sched_barrier(0);
-        for (int i0 = 0; i0 < mine; i0 += U) {
+    __builtin_amdgcn_sched_barrier(0);
+    v4i acc[MT];
+    int turn = 0, pass = 0, mine = 0;  // mine: the wave that ends the tile
+    for (int64_t left = tiles; left > 0;) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (i0 + u < mine) mul(ring[u]);
-                __builtin_amdgcn_sched_barrier(0);
-                load(ring[u], at(i0 + u + U));
-                __builtin_amdgcn_sched_barrier(0);
+        for (int d = 0; d < D; ++d) {
+            if (left > 0) {
+                if (!ONE) {
+                    load_rows(pass);
+                } else if (now.block != block) {
+                    load_rows(0);
+                    block = now.block;
+                }
+                if (ONE || pass == 0) {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) acc[m] = v4i{0, 0, 0, 0};
+                }
+#pragma unroll
+                for (int i = 0; i < NW; ++i) {
+                    const v4i w0 = ror8_into<0xC>(ring[d][i][0], ring[d][i][1]);
+                    const v4i w1 = ror8_into<0x3>(ring[d][i][1], ring[d][i][0]);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w0, a[i][m][0], acc[m], 0, 0, 0);
+                        acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w1, a[i][m][1], acc[m], 0, 0, 0);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                    load(ring[d], i);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (ONE || ++pass == passes) {
+                    pass = 0;
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) red[turn][wave][m][lane] = acc[m];
+                    // LDS done, the weights stay in flight; the other half of red was read before this
+                    // barrier by the waves that ended the tile before
+                    __asm__ volatile("" ::: "memory");
+                    __builtin_amdgcn_s_waitcnt(waitcnt(63, 0));
+                    __builtin_amdgcn_s_barrier();
+                    __asm__ volatile("" ::: "memory");
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        const bool me = mine == wave;
+                        mine = mine + 1 == W ? 0 : mine + 1;
+                        if (!me) continue;
+                        now.rows([&](auto src_row, int64_t slot0, int rows, const float *w_scale) {
+                            v4i s = red[turn][0][m][lane];
+                            for (int w = 1; w < W; ++w) s += red[turn][w][m][lane];
+                            // lane l: row 16 m + (l & 15), channels 4 (l >> 4) + r
+                            const int r0 = 16 * m + (lane & 15);
+                            if (r0 >= rows || src_row(r0) < 0) return;
+                            const int64_t nb = now.n0 + 4 * qd;
+                            T *o = out + (slot0 + r0) * ldo + nb;
+                            typedef T vt __attribute__((ext_vector_type(4)));
+                            vt v;
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const int64_t n = nb + r < N ? nb + r : N - 1;
+                                v[r] = finish<T>(s[r], as[m], w_scale[n], bias ? bias[n] : 0.0f, bias != nullptr);
+                            }
+                            if (vec && nb + 4 <= N) *reinterpret_cast<vt *>(o) = v;
+                            else {
+#pragma unroll
+                                for (int r = 0; r < 4; ++r)
+                                    if (nb + r < N) o[r] = v[r];
+                            }
+                        });
+                    }
+                    turn ^= 1;
+                    --left;
+                    if (left > 0) now.next();
+                }
             }
-        }
-    }
-    if (tail && wave == full % SPLIT) {  // chunks past K: any weights against zeros
-        Window x;
-        const int64_t k = (int64_t)full * 128;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int c = lane >> 3;
-            x.w[j] = *reinterpret_cast<const v4i *>(wp[j] + k + 16 * (c < tail ? c : 0));
-        }
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const int c = 2 * qd + s;
-                x.a[t][s] = *reinterpret_cast<const v4i *>(ap[t] + k + 16 * (c < tail ? c : 0));
-                if (c >= tail) x.a[t][s] = v4i{0, 0, 0, 0};
-            }
-        mul(x);
-    }
-#pragma unroll
-    for (int t = 0; t < MT; ++t) red[wave][t][lane] = acc[t];
-    __syncthreads();
-    // lane l of the wave that ends tile t holds row 16 t + (l & 15), channels 4 (l >> 4) + r
-    for (int t = wave; t < MT; t += SPLIT) {
-        v4i s = red[0][t][lane];
-#pragma unroll
-        for (int w = 1; w < SPLIT; ++w) s += red[w][t][lane];
-        const int m = 16 * t + (lane & 15);
-        const int64_t row = m < rows ? src_row(m) : -1;
-        if (row < 0) continue;
-        const float as = a_scale[row];
-        const int64_t nb = n0 + 4 * qd;
-        T *o = out + (slot0 + m) * ldo + nb;
-        typedef T vt __attribute__((ext_vector_type(4)));
-        vt v;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int64_t n = nb + r < N ? nb + r : N - 1;
-            v[r] = finish<T>(s[r], as, w_scale[n], bias ? bias[n] : 0.0f, bias != nullptr);
-        }
-        if (vec && nb + 4 <= N) *reinterpret_cast<vt *>(o) = v;
-        else {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (nb + r < N) o[r] = v[r];
         }
     }
 }
 
-template <int MT, int SPLIT, int U, typename T>
-__global__ __launch_bounds__(64 * SPLIT) void gemm_w8a8_stream_kernel(const int8_t *__restrict__ qa,
-                                                                      const float *__restrict__ a_scale, int64_t M,
-                                                                      int64_t K, const int8_t *__restrict__ qw,
-                                                                      const float *__restrict__ w_scale, int64_t N,
-                                                                      const float *__restrict__ bias,
-                                                                      T *__restrict__ out, int64_t ldo, bool vec) {
-    __shared__ v4i red[SPLIT][MT][64];
-    stream_unit<MT, SPLIT, U, T>(red, qa, a_scale, [](int r) { return (int64_t)r; }, 0, (int)M, K, qw, w_scale, N,
-                                 (int64_t)blockIdx.x * 16, bias, out, ldo, vec);
+// Workgroup b of g takes the tiles [begin(b), begin(b + 1)) of n: equal runs, the first ones longer.
+__device__ __forceinline__ int64_t run_begin(int64_t b, int64_t g, int64_t n) {
+    return n / g * b + (b < n % g ? b : n % g);
+}
+
+struct DenseWalk {
+    const int8_t *w;
+    int64_t bytes, n0, step, block;  // step: bytes of a tile
+    int rows_;
+    const float *w_scale;
+    __device__ void next() {
+        w += step;
+        bytes -= step;
+        n0 += 16;
+    }
+    template <typename F>
+    __device__ void rows(F f) const {
+        f([](int r) { return (int64_t)r; }, (int64_t)0, rows_, w_scale);
+    }
+};
+
+template <int MT, int NW, bool ONE, typename T>
+__global__ __launch_bounds__(64 * kMaxSliceWaves / MT) void gemm_w8a8_slice_kernel(
+    const int8_t *__restrict__ qa, const float *__restrict__ a_scale, int64_t M, int64_t K, int passes,
+    const int8_t *__restrict__ qw, const float *__restrict__ w_scale, int64_t N, const float *__restrict__ bias,
+    T *__restrict__ out, int64_t ldo, bool vec) {
+    __shared__ v4i red[2][kMaxSliceWaves][MT][64];
+    const int64_t nt = (N + 15) / 16, u0 = run_begin(blockIdx.x, gridDim.x, nt);
+    const DenseWalk walk{qw + u0 * 16 * K, (N - u0 * 16) * K, u0 * 16, 16 * K, 0, (int)M, w_scale};
+    slice_walk<MT, NW, ONE, T>(red, walk, run_begin(blockIdx.x + 1, gridDim.x, nt) - u0, qa, a_scale, K, passes, N,
+                               bias, out, ldo, vec);
 }
 
 // ------------------------------------------------------------------ per expert
@@ -506,25 +566,51 @@ __device__ __forceinline__ int find_expert(const int32_t *pfx, int32_t E, int32_
     return __builtin_amdgcn_readfirstlane(lo);  // u is the same for the whole workgroup
 }
 
-// Experts of up to 16 slots, a persistent grid over their 16-channel tiles.
-template <int SPLIT, int U>
-__global__ __launch_bounds__(64 * SPLIT) void grouped_w8a8_stream_kernel(
+struct ExpertWalk {
+    const int8_t *w;
+    int64_t bytes, n0, block;
+    int64_t e, K, N, R, max_slots;
+    int32_t E;
+    const int8_t *qw;
+    const float *w_scale;
+    const int32_t *pfx, *offsets, *row_index;
+    __device__ void at(int64_t b, int64_t n) {
+        block = b;
+        n0 = n;
+        e = find_expert(pfx, E, (int32_t)b);
+        w = qw + (e * N + n) * K;
+        bytes = (N - n) * K;
+    }
+    __device__ void next() {
+        n0 += 16;
+        w += 16 * K;
+        bytes -= 16 * K;
+        if (n0 >= N) at(block + 1, 0);
+    }
+    template <typename F>
+    __device__ void rows(F f) const {
+        const int64_t s0 = clamp_slots(offsets[e], max_slots) + 16 * (block - pfx[e]);
+        const int64_t left = clamp_slots(offsets[e + 1], max_slots) - s0;
+        f(SlotRows{row_index, s0, R}, s0, left < 16 ? (int)left : 16, w_scale + e * N);
+    }
+};
+
+// Experts of up to 16 slots: a workgroup's run of tiles goes through one expert after the other.
+template <int NW, bool ONE>
+__global__ __launch_bounds__(64 * kMaxSliceWaves) void grouped_w8a8_slice_kernel(
     const int8_t *__restrict__ qa, const float *__restrict__ a_scale, int64_t R, const int32_t *__restrict__ row_index,
-    const int32_t *__restrict__ offsets, int32_t E, int64_t K, const int8_t *__restrict__ qw,
+    const int32_t *__restrict__ offsets, int32_t E, int64_t K, int passes, const int8_t *__restrict__ qw,
     const float *__restrict__ w_scale, int64_t N, int64_t max_slots, int hi, float *__restrict__ out) {
-    __shared__ v4i red[SPLIT][1][64];
+    __shared__ v4i red[2][kMaxSliceWaves][1][64];
     __shared__ int32_t pfx[kPfx];
     block_prefix(pfx, offsets, E, max_slots, 0, hi, 16);
-    const int64_t nt = (N + 15) / 16, units = pfx[E] * nt;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int32_t b = (int32_t)(u / nt);
-        const int64_t e = find_expert(pfx, E, b);
-        const int64_t s0 = clamp_slots(offsets[e], max_slots) + 16 * (b - pfx[e]);
-        const int64_t left = clamp_slots(offsets[e + 1], max_slots) - s0;
-        stream_unit<1, SPLIT, U, float>(red, qa, a_scale, SlotRows{row_index, s0, R}, s0, left < 16 ? (int)left : 16, K,
-                                        qw + e * N * K, w_scale + e * N, N, u % nt * 16, nullptr, out, N, N % 4 == 0);
-        __syncthreads();  // red is taken again by the next unit
-    }
+    const int64_t nt = (N + 15) / 16, units = uniform(pfx[E]) * nt;
+    const int64_t u0 = run_begin(blockIdx.x, gridDim.x, units), u1 = run_begin(blockIdx.x + 1, gridDim.x, units);
+    if (u0 >= u1) return;
+    ExpertWalk walk{nullptr, 0, 0, 0, 0, K, N, R, max_slots, E, qw, w_scale, pfx, offsets, row_index};
+    const int64_t b = uniform(u0 / nt);
+    walk.at(b, uniform((u0 - b * nt) * 16));
+    slice_walk<1, NW, ONE, float>(red, walk, u1 - u0, qa, a_scale, K, passes, N, nullptr, out, N, N % 4 == 0);
 }
 
 // Experts with lo < slots <= hi on C's tiles: a persistent grid over (row block, column tile)
@@ -574,12 +660,43 @@ static hipError_t launch_tile(const int8_t *qa, const float *a_scale, int64_t M,
     return hipGetLastError();
 }
 
-template <int MT, int SPLIT, int U, typename T>
-static hipError_t launch_stream(const int8_t *qa, const float *a_scale, int64_t M, int64_t K, const int8_t *qw,
-                                const float *w_scale, int64_t N, const float *bias, T *out, int64_t ldo, bool vec,
-                                hipStream_t stream) {
-    hipLaunchKernelGGL((gemm_w8a8_stream_kernel<MT, SPLIT, U, T>), dim3((uint32_t)((N + 15) / 16)), dim3(64 * SPLIT), 0,
-                       stream, qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec);
+// How the few-row loop shares out k: waves, windows of each per pass, passes.  The fewest windows
+// that no wave needs (they cost cache reads), then the most waves.
+struct Slices {
+    int waves, nw, passes;
+};
+static Slices slices_of(int64_t K, int max_waves, int max_nw) {
+    const int64_t windows = (K + 127) / 128;
+    const int passes = (int)((windows + max_waves * max_nw - 1) / (max_waves * max_nw));
+    const int per = (int)((windows + passes - 1) / passes);
+    Slices best{1, max_nw, passes};
+    int waste = 1 << 30;
+    // several passes have one form, of max_nw windows
+    for (int nw = passes > 1 ? max_nw : 1; nw <= max_nw; ++nw) {
+        const int waves = (per + nw - 1) / nw;
+        if (waves <= max_waves && waves * nw - per < waste) {
+            waste = waves * nw - per;
+            best = Slices{waves, nw, passes};
+        }
+    }
+    return best;
+}
+
+template <int MT, typename T>
+static hipError_t launch_slice(const int8_t *qa, const float *a_scale, int64_t M, int64_t K, const int8_t *qw,
+                               const float *w_scale, int64_t N, const float *bias, T *out, int64_t ldo, bool vec,
+                               hipStream_t stream) {
+    const Slices s = slices_of(K, kMaxSliceWaves / MT, 4);
+    const int64_t grid = std::min<int64_t>((N + 15) / 16, kCus * (kMaxSliceWaves / MT / s.waves));
+#define W4A8_SLICE(NN, ONE)                                                                                         \
+    hipLaunchKernelGGL((gemm_w8a8_slice_kernel<MT, NN, ONE, T>), dim3((uint32_t)grid), dim3(64 * s.waves), 0, stream, \
+                       qa, a_scale, M, K, s.passes, qw, w_scale, N, bias, out, ldo, vec)
+    if (s.passes > 1) W4A8_SLICE(4, false);
+    else if (s.nw == 1) W4A8_SLICE(1, true);
+    else if (s.nw == 2) W4A8_SLICE(2, true);
+    else if (s.nw == 3) W4A8_SLICE(3, true);
+    else W4A8_SLICE(4, true);
+#undef W4A8_SLICE
     return hipGetLastError();
 }
 
@@ -588,8 +705,8 @@ static hipError_t gemm_w8a8_typed(const int8_t *qa, const float *a_scale, int64_
                                   const float *w_scale, int64_t N, const float *bias, T *out, int64_t ldo,
                                   hipStream_t stream) {
     const bool vec = (uintptr_t)out % 16 == 0 && ldo * (int64_t)sizeof(T) % 16 == 0;
-    if (M <= 16) return launch_stream<1, 8, 4>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream);
-    if (M <= 32) return launch_stream<2, 8, 4>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream);
+    if (M <= 16) return launch_slice<1>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream);
+    if (M <= 32) return launch_slice<2>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream);
     if (M <= 64) return launch_tile<Tile64>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream);
     if (M <= 128) return launch_tile<Tile128>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream);
     return launch_tile<Tile256>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream);
@@ -626,15 +743,23 @@ hipError_t launch_grouped_gemm_w8a8(const int8_t *qa, const float *a_scale, int6
                                     const int32_t *expert_offsets, int32_t E, int64_t K, const int8_t *qw,
                                     const float *w_scale, int64_t N, int64_t max_slots, float *out,
                                     hipStream_t stream) {
-    constexpr int SPLIT = 8, kStreamMax = 16, kTile64Max = 64;
+    constexpr int kFewMax = 16, kTile64Max = 64;
+    const Slices s = slices_of(K, kMaxSliceWaves, 4);
     const int64_t units = std::min<int64_t>(E, max_slots) * ((N + 15) / 16);
-    const int64_t grid = std::min<int64_t>(units, kCus * 4);
-    hipLaunchKernelGGL((grouped_w8a8_stream_kernel<SPLIT, 4>), dim3((uint32_t)grid), dim3(64 * SPLIT), 0, stream, qa,
-                       a_scale, R, row_index, expert_offsets, E, K, qw, w_scale, N, max_slots, kStreamMax, out);
+    const int64_t grid = std::min<int64_t>(units, kCus * (kMaxSliceWaves / s.waves));
+#define W4A8_SLICE(NN, ONE)                                                                                       \
+    hipLaunchKernelGGL((grouped_w8a8_slice_kernel<NN, ONE>), dim3((uint32_t)grid), dim3(64 * s.waves), 0, stream, \
+                       qa, a_scale, R, row_index, expert_offsets, E, K, s.passes, qw, w_scale, N, max_slots, kFewMax, out)
+    if (s.passes > 1) W4A8_SLICE(4, false);
+    else if (s.nw == 1) W4A8_SLICE(1, true);
+    else if (s.nw == 2) W4A8_SLICE(2, true);
+    else if (s.nw == 3) W4A8_SLICE(3, true);
+    else W4A8_SLICE(4, true);
+#undef W4A8_SLICE
     hipError_t err = hipGetLastError();
-    if (err == hipSuccess && max_slots > kStreamMax)
+    if (err == hipSuccess && max_slots > kFewMax)
         err = launch_grouped_tile<Tile64>(qa, a_scale, R, row_index, expert_offsets, E, K, qw, w_scale, N, max_slots,
-                                          kStreamMax, kTile64Max, out, stream);
+                                          kFewMax, kTile64Max, out, stream);
     if (err == hipSuccess && max_slots > kTile64Max)
         err = launch_grouped_tile<Tile128>(qa, a_scale, R, row_index, expert_offsets, E, K, qw, w_scale, N, max_slots,
                                            kTile64Max, 0x7FFFFFFF, out, stream);
