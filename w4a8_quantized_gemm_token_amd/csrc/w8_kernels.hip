@@ -74,8 +74,10 @@ struct Tile {
 };
 
 // src_row(r), r < rows: activation row of the tile's row r, or -1 (computed as row 0, not stored).
-// VEC: output rows start 16-byte aligned.
-template <typename C, typename T, typename SrcRow>
+// vec: output rows start 16-byte aligned.  WIDE: rows may lie 2^32 bytes or more behind qa.  (Its
+// loads take 64-bit addresses, and the compiler counts those as able to touch LDS by themselves:
+// it then waits for every access in flight where it would wait for some.)
+template <typename C, bool WIDE, typename T, typename SrcRow>
 __device__ __forceinline__ void tile_unit(uint8_t *lds, const int8_t *__restrict__ qa,
                                           const float *__restrict__ a_scale, SrcRow src_row, int64_t slot0, int rows,
                                           int64_t K, const int8_t *__restrict__ qw,
@@ -89,16 +91,18 @@ __device__ __forceinline__ void tile_unit(uint8_t *lds, const int8_t *__restrict
     constexpr int kReads = C::RB + C::CB, kMul = C::RB * C::CB, kLoads = C::LA + C::LB;
 
     // ---- loads: lane L of load j fills chunk L & 7 of row 8 (L? wave + j) + (L >> 3)
-    const int8_t *aptr[C::LA];
-    uint32_t boff[C::LB];
+    const int8_t *aptr[WIDE ? C::LA : 1];
+    uint32_t aoff[C::LA], boff[C::LB];
     int ach[C::LA], bch[C::LB];
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(qa);
 #pragma unroll
     for (int j = 0; j < C::LA; ++j) {
         const int r = 8 * (C::LA * wave + j) + (lane >> 3);
         int64_t src = src_row(r < rows ? r : rows - 1);
         if (src < 0) src = 0;
         ach[j] = (lane & 7) ^ C::key_a(r);
-        aptr[j] = qa + src * K + 16 * ach[j];
+        if constexpr (WIDE) aptr[j] = qa + src * K + 16 * ach[j];
+        else aoff[j] = (uint32_t)src * (uint32_t)K + 16u * (uint32_t)ach[j];
     }
     const __amdgpu_buffer_rsrc_t rb = make_rsrc((const void *)uniform((int64_t)(qw + n0 * K)));
 #pragma unroll
@@ -109,14 +113,17 @@ __device__ __forceinline__ void tile_unit(uint8_t *lds, const int8_t *__restrict
         boff[j] = (uint32_t)(c * K) + 16u * (uint32_t)bch[j];
     }
     auto load_one = [&](int g, int st, int j) {  // load j of a whole stage
-        if (j < C::LB)
+        if (j < C::LB) {
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 rb, (lds_ptr_t)(lds + st * C::kStage + C::kStageA + 1024 * (C::LB * wave + j)), 16, (int)boff[j % C::LB],
                 g * 128, 0, 0);
-        else
-            __builtin_amdgcn_global_load_lds((glb_ptr_t)(aptr[(j - C::LB) % C::LA] + (int64_t)g * 128),
-                                             (lds_ptr_t)(lds + st * C::kStage + 1024 * (C::LA * wave + j - C::LB)), 16, 0,
-                                             0);
+        } else {
+            const int i = (j - C::LB) % C::LA;
+            const lds_ptr_t to = (lds_ptr_t)(lds + st * C::kStage + 1024 * (C::LA * wave + i));
+            if constexpr (WIDE)
+                __builtin_amdgcn_global_load_lds((glb_ptr_t)(aptr[i] + (int64_t)g * 128), to, 16, 0, 0);
+            else __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, to, 16, (int)aoff[i], g * 128, 0, 0);
+        }
     };
     auto issue = [&](int g, int st) {
         if (g < full) {
@@ -285,8 +292,10 @@ __device__ __forceinline__ void panel_tile(int64_t b, int64_t mt, int64_t nt, in
     tn = ip / pm;
 }
 
+// (256 threads: two waves per SIMD are asked for, or the compiler spreads over 512 registers and moves
+// accumulators about.)
 template <typename C, typename T>
-__global__ __launch_bounds__(C::kThreads) void gemm_w8a8_tile_kernel(const int8_t *__restrict__ qa,
+__global__ __launch_bounds__(C::kThreads, C::kThreads == 256 ? 2 : 1) void gemm_w8a8_tile_kernel(const int8_t *__restrict__ qa,
                                                                      const float *__restrict__ a_scale, int64_t M,
                                                                      int64_t K, const int8_t *__restrict__ qw,
                                                                      const float *__restrict__ w_scale, int64_t N,
@@ -298,12 +307,12 @@ __global__ __launch_bounds__(C::kThreads) void gemm_w8a8_tile_kernel(const int8_
     panel_tile<4>(blockIdx.x, mt, nt, tm, tn);
     const int64_t m0 = tm * C::BM;
     const int rows = (int)((M - m0) < C::BM ? (M - m0) : C::BM);
-    tile_unit<C, T>(lds, qa, a_scale, [&](int r) { return m0 + r; }, m0, rows, K, qw, w_scale, N, tn * C::BN, bias, out,
-                    ldo, vec);
+    tile_unit<C, false, T>(lds, qa + m0 * K, a_scale + m0, [](int r) { return (int64_t)r; }, m0, rows, K, qw, w_scale, N,
+                           tn * C::BN, bias, out, ldo, vec);
 }
 
 // ------------------------------------------------------------------ few rows
-// Up to 16 MT rows: the weights are the whole cost, and each byte of them is used once.  A
+// Up to 16 rows: the weights are the whole cost, and each byte of them is used once.  A
 // workgroup's waves share out k in 128-byte windows (wave w has the windows w + W i, i < NW, of
 // a pass of W NW windows; one pass where K allows) and walk the same run of 16-channel tiles, so
 // a wave keeps its slice of the activations in registers for the whole run and does nothing but
@@ -330,8 +339,8 @@ constexpr int kMaxSliceWaves = 16;
 // tile's first channel, and from there to the end of the array's or the expert's last row), n0
 // (the first channel), block (the rows stay in registers while it stays), next(), and rows(f),
 // which calls f(src_row, slot0, rows, w_scale).  ONE: a single pass.
-template <int MT, int NW, bool ONE, typename T, typename Walk>
-__device__ __forceinline__ void slice_walk(v4i (*red)[kMaxSliceWaves][MT][64], Walk to_load, int64_t tiles,
+template <int NW, bool ONE, typename T, typename Walk>
+__device__ __forceinline__ void slice_walk(v4i (*red)[kMaxSliceWaves][64], Walk to_load, int64_t tiles,
                                            const int8_t *__restrict__ qa, const float *__restrict__ a_scale, int64_t K,
                                            int passes, int64_t N, const float *__restrict__ bias, T *__restrict__ out,
                                            int64_t ldo, bool vec) {
@@ -343,7 +352,7 @@ __device__ __forceinline__ void slice_walk(v4i (*red)[kMaxSliceWaves][MT][64], W
     const uint32_t lofs = (uint32_t)(lane & 7) * (uint32_t)K + 16u * (uint32_t)(lane >> 3), row8 = 8u * (uint32_t)K;
     Walk now = to_load;  // the tile of the products; to_load is D steps ahead
 
-    v4i a[NW][MT][2], ring[D][NW][2];
+    v4i a[NW][2], ring[D][NW][2];
     int64_t loaded = 0;
     int load_pass = 0;
     auto load = [&](v4i (&x)[NW][2], int i) {  // window i of the next tile (or pass) to load
@@ -362,25 +371,21 @@ __device__ __forceinline__ void slice_walk(v4i (*red)[kMaxSliceWaves][MT][64], W
         load_pass = 0;
         if (++loaded < tiles) to_load.next();
     };
-    float as[MT];
+    float as = 0.0f;
     auto load_rows = [&](int pass) {
         now.rows([&](auto src_row, int64_t, int rows, const float *) {
+            int64_t src = src_row((lane & 15) < rows ? lane & 15 : rows - 1);
+            src = src < 0 ? 0 : src;
+            as = a_scale[src];
+            const int8_t *p = qa + src * K;
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                const int r = 16 * t + (lane & 15);
-                int64_t src = src_row(r < rows ? r : rows - 1);
-                src = src < 0 ? 0 : src;
-                as[t] = a_scale[src];
-                const int8_t *p = qa + src * K;
+            for (int i = 0; i < NW; ++i) {
+                const int w = (pass * NW + i) * W + wave;
 #pragma unroll
-                for (int i = 0; i < NW; ++i) {
-                    const int w = (pass * NW + i) * W + wave;
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const int64_t k = (int64_t)w * 128 + 32 * qd + 16 * s;
-                        const v4i v = *reinterpret_cast<const v4i *>(p + (k < K ? k : 0));
-                        a[i][t][s] = k < K ? v : v4i{0, 0, 0, 0};
-                    }
+                for (int s = 0; s < 2; ++s) {
+                    const int64_t k = (int64_t)w * 128 + 32 * qd + 16 * s;
+                    const v4i v = *reinterpret_cast<const v4i *>(p + (k < K ? k : 0));
+                    a[i][s] = k < K ? v : v4i{0, 0, 0, 0};
                 }
             }
         });
@@ -395,7 +400,7 @@ __device__ __forceinline__ void slice_walk(v4i (*red)[kMaxSliceWaves][MT][64], W
             load(ring[d], i);
         }
     __builtin_amdgcn_sched_barrier(0);
-    v4i acc[MT];
+    v4i acc = {};
     int turn = 0, pass = 0, mine = 0;  // mine: the wave that ends the tile
     for (int64_t left = tiles; left > 0;) {
 #pragma unroll
@@ -407,52 +412,41 @@ __device__ __forceinline__ void slice_walk(v4i (*red)[kMaxSliceWaves][MT][64], W
                     load_rows(0);
                     block = now.block;
                 }
-                if (ONE || pass == 0) {
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) acc[m] = v4i{0, 0, 0, 0};
-                }
+                if (ONE || pass == 0) acc = v4i{0, 0, 0, 0};
 #pragma unroll
                 for (int i = 0; i < NW; ++i) {
                     const v4i w0 = ror8_into<0xC>(ring[d][i][0], ring[d][i][1]);
                     const v4i w1 = ror8_into<0x3>(ring[d][i][1], ring[d][i][0]);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w0, a[i][m][0], acc[m], 0, 0, 0);
-                        acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w1, a[i][m][1], acc[m], 0, 0, 0);
-                    }
+                    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w0, a[i][0], acc, 0, 0, 0);
+                    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w1, a[i][1], acc, 0, 0, 0);
                     __builtin_amdgcn_sched_barrier(0);
                     load(ring[d], i);
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 if (ONE || ++pass == passes) {
                     pass = 0;
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) red[turn][wave][m][lane] = acc[m];
+red[turn][wave][lane] = acc;
                     // LDS done, the weights stay in flight; the other half of red was read before this
-                    // barrier by the waves that ended the tile before
+                    // barrier by the wave that ended the tile before
                     __asm__ volatile("" ::: "memory");
                     __builtin_amdgcn_s_waitcnt(waitcnt(63, 0));
                     __builtin_amdgcn_s_barrier();
                     __asm__ volatile("" ::: "memory");
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        const bool me = mine == wave;
-                        mine = mine + 1 == W ? 0 : mine + 1;
-                        if (!me) continue;
+                    if (mine == wave)
                         now.rows([&](auto src_row, int64_t slot0, int rows, const float *w_scale) {
-                            v4i s = red[turn][0][m][lane];
-                            for (int w = 1; w < W; ++w) s += red[turn][w][m][lane];
-                            // lane l: row 16 m + (l & 15), channels 4 (l >> 4) + r
-                            const int r0 = 16 * m + (lane & 15);
-                            if (r0 >= rows || src_row(r0) < 0) return;
+                            v4i s = red[turn][0][lane];
+                            for (int w = 1; w < W; ++w) s += red[turn][w][lane];
+                            // lane l: row l & 15, channels 4 (l >> 4) + r
+                            const int m = lane & 15;
+                            if (m >= rows || src_row(m) < 0) return;
                             const int64_t nb = now.n0 + 4 * qd;
-                            T *o = out + (slot0 + r0) * ldo + nb;
+                            T *o = out + (slot0 + m) * ldo + nb;
                             typedef T vt __attribute__((ext_vector_type(4)));
                             vt v;
 #pragma unroll
                             for (int r = 0; r < 4; ++r) {
                                 const int64_t n = nb + r < N ? nb + r : N - 1;
-                                v[r] = finish<T>(s[r], as[m], w_scale[n], bias ? bias[n] : 0.0f, bias != nullptr);
+                                v[r] = finish<T>(s[r], as, w_scale[n], bias ? bias[n] : 0.0f, bias != nullptr);
                             }
                             if (vec && nb + 4 <= N) *reinterpret_cast<vt *>(o) = v;
                             else {
@@ -461,7 +455,7 @@ __device__ __forceinline__ void slice_walk(v4i (*red)[kMaxSliceWaves][MT][64], W
                                     if (nb + r < N) o[r] = v[r];
                             }
                         });
-                    }
+                    mine = mine + 1 == W ? 0 : mine + 1;
                     turn ^= 1;
                     --left;
                     if (left > 0) now.next();
@@ -492,15 +486,15 @@ struct DenseWalk {
     }
 };
 
-template <int MT, int NW, bool ONE, typename T>
-__global__ __launch_bounds__(64 * kMaxSliceWaves / MT) void gemm_w8a8_slice_kernel(
+template <int NW, bool ONE, typename T>
+__global__ __launch_bounds__(64 * kMaxSliceWaves) void gemm_w8a8_slice_kernel(
     const int8_t *__restrict__ qa, const float *__restrict__ a_scale, int64_t M, int64_t K, int passes,
     const int8_t *__restrict__ qw, const float *__restrict__ w_scale, int64_t N, const float *__restrict__ bias,
     T *__restrict__ out, int64_t ldo, bool vec) {
-    __shared__ v4i red[2][kMaxSliceWaves][MT][64];
+    __shared__ v4i red[2][kMaxSliceWaves][64];
     const int64_t nt = (N + 15) / 16, u0 = run_begin(blockIdx.x, gridDim.x, nt);
     const DenseWalk walk{qw + u0 * 16 * K, (N - u0 * 16) * K, u0 * 16, 16 * K, 0, (int)M, w_scale};
-    slice_walk<MT, NW, ONE, T>(red, walk, run_begin(blockIdx.x + 1, gridDim.x, nt) - u0, qa, a_scale, K, passes, N,
+    slice_walk<NW, ONE, T>(red, walk, run_begin(blockIdx.x + 1, gridDim.x, nt) - u0, qa, a_scale, K, passes, N,
                                bias, out, ldo, vec);
 }
 
@@ -601,7 +595,7 @@ __global__ __launch_bounds__(64 * kMaxSliceWaves) void grouped_w8a8_slice_kernel
     const int8_t *__restrict__ qa, const float *__restrict__ a_scale, int64_t R, const int32_t *__restrict__ row_index,
     const int32_t *__restrict__ offsets, int32_t E, int64_t K, int passes, const int8_t *__restrict__ qw,
     const float *__restrict__ w_scale, int64_t N, int64_t max_slots, int hi, float *__restrict__ out) {
-    __shared__ v4i red[2][kMaxSliceWaves][1][64];
+    __shared__ v4i red[2][kMaxSliceWaves][64];
     __shared__ int32_t pfx[kPfx];
     block_prefix(pfx, offsets, E, max_slots, 0, hi, 16);
     const int64_t nt = (N + 15) / 16, units = uniform(pfx[E]) * nt;
@@ -610,22 +604,22 @@ __global__ __launch_bounds__(64 * kMaxSliceWaves) void grouped_w8a8_slice_kernel
     ExpertWalk walk{nullptr, 0, 0, 0, 0, K, N, R, max_slots, E, qw, w_scale, pfx, offsets, row_index};
     const int64_t b = uniform(u0 / nt);
     walk.at(b, uniform((u0 - b * nt) * 16));
-    slice_walk<1, NW, ONE, float>(red, walk, u1 - u0, qa, a_scale, K, passes, N, nullptr, out, N, N % 4 == 0);
+    slice_walk<NW, ONE, float>(red, walk, u1 - u0, qa, a_scale, K, passes, N, nullptr, out, N, N % 4 == 0);
 }
 
-// Experts with lo < slots <= hi on C's tiles: a persistent grid over (row block, column tile)
+// Experts with more than lo slots on C's tiles: a persistent grid over (row block, column tile)
 // units, an expert's row blocks next to each other on one XCD, so that its weights come
 // through one L2.
 template <typename C>
 __global__ __launch_bounds__(C::kThreads) void grouped_w8a8_tile_kernel(
     const int8_t *__restrict__ qa, const float *__restrict__ a_scale, int64_t R, const int32_t *__restrict__ row_index,
     const int32_t *__restrict__ offsets, int32_t E, int64_t K, const int8_t *__restrict__ qw,
-    const float *__restrict__ w_scale, int64_t N, int64_t max_slots, int lo, int hi, float *__restrict__ out) {
+    const float *__restrict__ w_scale, int64_t N, int64_t max_slots, int lo, float *__restrict__ out) {
     // one LDS object: with several, the compiler tells the loads into LDS and the reads apart by
     // object and puts a wait for every load in flight before the reads of the stages
     __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kLds + kPfx * 4];
     int32_t *pfx = reinterpret_cast<int32_t *>(lds + C::kLds);
-    block_prefix(pfx, offsets, E, max_slots, lo, hi, C::BM);
+    block_prefix(pfx, offsets, E, max_slots, lo, 0x7FFFFFFF, C::BM);
     const int64_t nt = (N + C::BN - 1) / C::BN, units = pfx[E] * nt;
     const int64_t per = gridDim.x / 8;  // the grid is a multiple of 8
     for (int64_t u = blockIdx.x % 8 * per + blockIdx.x / 8; u < units; u += gridDim.x) {
@@ -635,7 +629,7 @@ __global__ __launch_bounds__(C::kThreads) void grouped_w8a8_tile_kernel(
         const int64_t b = (u - p0 * nt) % nb, tn = (u - p0 * nt) / nb;
         const int64_t s0 = clamp_slots(offsets[e], max_slots) + C::BM * b;
         const int64_t left = clamp_slots(offsets[e + 1], max_slots) - s0;
-        tile_unit<C, float>(lds, qa, a_scale, SlotRows{row_index, s0, R}, s0, left < C::BM ? (int)left : C::BM, K,
+        tile_unit<C, true, float>(lds, qa, a_scale, SlotRows{row_index, s0, R}, s0, left < C::BM ? (int)left : C::BM, K,
                             qw + e * N * K, w_scale + e * N, N, tn * C::BN, nullptr, out, N, N % 4 == 0);
         __syncthreads();  // the LDS stages are taken again by the next unit
     }
@@ -643,7 +637,9 @@ __global__ __launch_bounds__(C::kThreads) void grouped_w8a8_tile_kernel(
 
 using Tile256 = Tile<256, 256, 2, 4, 2>;
 using Tile128 = Tile<128, 256, 2, 4, 3>;
-using Tile64 = Tile<64, 256, 2, 4, 3>;
+using Tile128n = Tile<128, 128, 2, 4, 4>;
+using Tile64 = Tile<64, 64, 2, 2, 4>;  // two workgroups per CU, as the next
+using Tile32 = Tile<32, 64, 2, 2, 6>;
 constexpr int kCus = 256;
 
 }  // namespace
@@ -682,14 +678,14 @@ static Slices slices_of(int64_t K, int max_waves, int max_nw) {
     return best;
 }
 
-template <int MT, typename T>
+template <typename T>
 static hipError_t launch_slice(const int8_t *qa, const float *a_scale, int64_t M, int64_t K, const int8_t *qw,
                                const float *w_scale, int64_t N, const float *bias, T *out, int64_t ldo, bool vec,
                                hipStream_t stream) {
-    const Slices s = slices_of(K, kMaxSliceWaves / MT, 4);
-    const int64_t grid = std::min<int64_t>((N + 15) / 16, kCus * (kMaxSliceWaves / MT / s.waves));
+    const Slices s = slices_of(K, kMaxSliceWaves, 4);
+    const int64_t grid = std::min<int64_t>((N + 15) / 16, kCus * (kMaxSliceWaves / s.waves));
 #define W4A8_SLICE(NN, ONE)                                                                                         \
-    hipLaunchKernelGGL((gemm_w8a8_slice_kernel<MT, NN, ONE, T>), dim3((uint32_t)grid), dim3(64 * s.waves), 0, stream, \
+    hipLaunchKernelGGL((gemm_w8a8_slice_kernel<NN, ONE, T>), dim3((uint32_t)grid), dim3(64 * s.waves), 0, stream, \
                        qa, a_scale, M, K, s.passes, qw, w_scale, N, bias, out, ldo, vec)
     if (s.passes > 1) W4A8_SLICE(4, false);
     else if (s.nw == 1) W4A8_SLICE(1, true);
@@ -705,11 +701,25 @@ static hipError_t gemm_w8a8_typed(const int8_t *qa, const float *a_scale, int64_
                                   const float *w_scale, int64_t N, const float *bias, T *out, int64_t ldo,
                                   hipStream_t stream) {
     const bool vec = (uintptr_t)out % 16 == 0 && ldo * (int64_t)sizeof(T) % 16 == 0;
-    if (M <= 16) return launch_slice<1>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream);
-    if (M <= 32) return launch_slice<2>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream);
-    if (M <= 64) return launch_tile<Tile64>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream);
-    if (M <= 128) return launch_tile<Tile128>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream);
-    return launch_tile<Tile256>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream);
+    // Few rows and a long k, or runs of at least four 16-channel tiles for every workgroup: k shared
+    // out within the workgroup (K 16384, N 4096, one row: 18.7 us against 24.3 on 32 x 64 tiles;
+    // K 4096, N 14336: 17.7 against 14.3).
+    if (M <= 16 && (K > 8192 || N >= 16 * 4 * kCus))
+        return launch_slice(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream);
+    // Else the largest tile that nearly fills the CUs (and is no taller than M needs): a tile of 16
+    // times the area reads a quarter of the bytes per product, but 64 idle CUs of 256 cost more.
+    // M 512, K = N 8192: 128 x 128 (256 tiles) 41 us, 128 x 256 58, 64 x 64 68; M 77, K 4112, N 5003:
+    // 32 x 64 (237) 10 us, 64 x 64 (158) 14, 128 x 128 22.
+    auto fits = [&](int64_t bm, int64_t bn) {
+        return bm < 2 * M && ((M + bm - 1) / bm) * ((N + bn - 1) / bn) >= kCus * 7 / 8;
+    };
+#define W4A8_TILE(C) launch_tile<C>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream)
+    if (fits(256, 256)) return W4A8_TILE(Tile256);
+    if (fits(128, 256)) return W4A8_TILE(Tile128);
+    if (fits(128, 128)) return W4A8_TILE(Tile128n);
+    if (fits(64, 64)) return W4A8_TILE(Tile64);
+    return W4A8_TILE(Tile32);
+#undef W4A8_TILE
 }
 
 hipError_t launch_gemm_w8a8(const int8_t *qa, const float *a_scale, int64_t M, int64_t K, const int8_t *qw,
@@ -728,14 +738,14 @@ hipError_t launch_gemm_w8a8(const int8_t *qa, const float *a_scale, int64_t M, i
 template <typename C>
 static hipError_t launch_grouped_tile(const int8_t *qa, const float *a_scale, int64_t R, const int32_t *row_index,
                                       const int32_t *offsets, int32_t E, int64_t K, const int8_t *qw,
-                                      const float *w_scale, int64_t N, int64_t max_slots, int lo, int hi, float *out,
+                                      const float *w_scale, int64_t N, int64_t max_slots, int lo, float *out,
                                       hipStream_t stream) {
     // the most units there can be: every expert of the class has more than lo slots
     const int64_t blocks = std::min<int64_t>((int64_t)E, max_slots / (lo + 1)) + max_slots / C::BM;
     const int64_t units = blocks * ((N + C::BN - 1) / C::BN);
     const int64_t grid = std::min<int64_t>((units + 7) / 8 * 8, kCus);
     hipLaunchKernelGGL((grouped_w8a8_tile_kernel<C>), dim3((uint32_t)grid), dim3(C::kThreads), 0, stream, qa, a_scale, R,
-                       row_index, offsets, E, K, qw, w_scale, N, max_slots, lo, hi, out);
+                       row_index, offsets, E, K, qw, w_scale, N, max_slots, lo, out);
     return hipGetLastError();
 }
 
@@ -743,7 +753,7 @@ hipError_t launch_grouped_gemm_w8a8(const int8_t *qa, const float *a_scale, int6
                                     const int32_t *expert_offsets, int32_t E, int64_t K, const int8_t *qw,
                                     const float *w_scale, int64_t N, int64_t max_slots, float *out,
                                     hipStream_t stream) {
-    constexpr int kFewMax = 16, kTile64Max = 64;
+    constexpr int kFewMax = 16;
     const Slices s = slices_of(K, kMaxSliceWaves, 4);
     const int64_t units = std::min<int64_t>(E, max_slots) * ((N + 15) / 16);
     const int64_t grid = std::min<int64_t>(units, kCus * (kMaxSliceWaves / s.waves));
@@ -758,11 +768,8 @@ hipError_t launch_grouped_gemm_w8a8(const int8_t *qa, const float *a_scale, int6
 #undef W4A8_SLICE
     hipError_t err = hipGetLastError();
     if (err == hipSuccess && max_slots > kFewMax)
-        err = launch_grouped_tile<Tile64>(qa, a_scale, R, row_index, expert_offsets, E, K, qw, w_scale, N, max_slots,
-                                          kFewMax, kTile64Max, out, stream);
-    if (err == hipSuccess && max_slots > kTile64Max)
         err = launch_grouped_tile<Tile128>(qa, a_scale, R, row_index, expert_offsets, E, K, qw, w_scale, N, max_slots,
-                                           kTile64Max, 0x7FFFFFFF, out, stream);
+                                           kFewMax, out, stream);
     return err;
 }
 
