@@ -39,43 +39,66 @@ __device__ __forceinline__ double wave_sum64(double v) {
     return v;
 }
 
+// Minimum over the wave, returned to every lane (DPP inside each 16-lane row, then the four rows).
+template <int CTRL>
+__device__ __forceinline__ int dpp_min(int v) {
+    return min(v, __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ int wave_min_int(int v) {
+    v = dpp_min<0xB1>(v);   // quad_perm [1,0,3,2]
+    v = dpp_min<0x4E>(v);   // quad_perm [2,3,0,1]
+    v = dpp_min<0x124>(v);  // row_ror:4
+    v = dpp_min<0x128>(v);  // row_ror:8
+    return min(min(__builtin_amdgcn_readlane(v, 0), __builtin_amdgcn_readlane(v, 16)),
+               min(__builtin_amdgcn_readlane(v, 32), __builtin_amdgcn_readlane(v, 48)));
+}
+__device__ __forceinline__ double readlane64(double v, int l) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)b, l), hi = __builtin_amdgcn_readlane((int)(b >> 32), l);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
 // Orders a wave's LDS writes before its other lanes' reads (LDS runs a wave's accesses in order;
 // this keeps the compiler from moving them).
 __device__ __forceinline__ void wave_lds_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
-// One wave per token; lane l holds experts l, l + 64, ... (PER of them).
+// Routes one token with one wave; lane l holds experts l, l + 64, ... (PER of them).
+// A pick is the wave's largest key: each lane keeps its own best open key in fp64 and that rounded
+// to fp32; the rounding keeps the order, so the fp32 maximum (a few DPP steps) names the winner
+// unless several lanes share it, and only those are then compared in fp64, and by id.
+// val, gval: the wave's own LDS, used when there are groups.
 template <int PER, typename L>
-__global__ __launch_bounds__(kRouteThreads) void route_scored_kernel(const L *__restrict__ logits, int64_t ldl,
-                                                                     const float *__restrict__ bias, int64_t T,
-                                                                     int32_t E, RouteCfg c, int32_t *__restrict__ ids,
-                                                                     float *__restrict__ w) {
-    __shared__ double val[kRouteWaves][PER * kWave];
-    __shared__ double gval[kRouteWaves][w4a8::kMaxRouteGroups];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
-    if (t >= T) return;  // whole waves; the LDS rows are each wave's own
-    const L *row = logits + t * ldl;
-    float x[PER];
+__device__ __forceinline__ void route_scored_token(const L *__restrict__ row, const float *__restrict__ bias, int32_t E,
+                                                   const RouteCfg &c, double *val, double *gval,
+                                                   int32_t *__restrict__ ids, float *__restrict__ w) {
+    const int lane = threadIdx.x & 63;
+    float x[PER], b[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int e = i * kWave + lane;
         x[i] = e < E ? tame(logit_at(row, e)) : -INFINITY;
+        b[i] = bias && e < E ? tame(bias[e]) : 0.0f;
     }
-    float top = -INFINITY;
+    const bool softmax = c.score == W4A8_SCORE_SOFTMAX;
+    double top = 0.0, denom = 1.0;
+    if (softmax) {
+        float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) top = fmaxf(top, x[i]);
-    top = wave_max(top);
-    double denom = 1.0;
-    if (c.score == W4A8_SCORE_SOFTMAX && top > -INFINITY) {
-        double sum = 0.0;
+        for (int i = 0; i < PER; ++i) m = fmaxf(m, x[i]);
+        m = wave_max(m);
+        if (m > -INFINITY) {
+            top = (double)m;
+            double sum = 0.0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) sum += exp((double)x[i] - (double)top);
-        denom = wave_sum64(sum);
+            for (int i = 0; i < PER; ++i) sum += exp((double)x[i] - top);
+            denom = wave_sum64(sum);
+        }
     }
     auto score = [&](float xv) -> double {
         if (!(xv > -INFINITY)) return 0.0;
-        return c.score == W4A8_SCORE_SOFTMAX ? exp((double)xv - (double)top) / denom : sigmoid64(xv);
+        return softmax ? exp((double)xv - top) / denom : sigmoid64(xv);
     };
+    const bool scored = bias || c.n_groups > 1;  // else the logits themselves are the keys
     double key[PER];
     uint32_t taken = 0;  // bit i: expert i * 64 + lane is picked, outside E or in a closed group
 #pragma unroll
@@ -83,38 +106,37 @@ __global__ __launch_bounds__(kRouteThreads) void route_scored_kernel(const L *__
         const int e = i * kWave + lane;
         if (e >= E) taken |= 1u << i;
         double v = -INFINITY;
-        const float b = bias && e < E ? tame(bias[e]) : 0.0f;
-        if (x[i] > -INFINITY && b > -INFINITY && (bias || c.n_groups > 1)) v = score(x[i]) + (double)b;
-        if (c.n_groups > 1) val[wave][i * kWave + lane] = v;
+        if (scored && x[i] > -INFINITY && b[i] > -INFINITY) v = score(x[i]) + (double)b[i];
+        if (c.n_groups > 1) val[i * kWave + lane] = v;
         key[i] = bias ? v : (double)x[i];
     }
     if (c.n_groups > 1) {
-        // 64 / n_groups lanes (a power of two) walk each group, their best two are merged
+        // 64 / n_groups lanes (a power of two) walk each group; their best two are merged
         wave_lds_fence();
         const int gs = E / c.n_groups;
         int seg = 1;
         while (2 * seg * c.n_groups <= kWave) seg *= 2;
         const int g = lane / seg;
-        double a = -INFINITY, b = -INFINITY;
+        double v1 = -INFINITY, v2 = -INFINITY;
         if (g < c.n_groups)
             for (int j = lane % seg; j < gs; j += seg) {
-                const double v = val[wave][g * gs + j];
-                b = fmax(b, fmin(a, v));
-                a = fmax(a, v);
+                const double v = val[g * gs + j];
+                v2 = fmax(v2, fmin(v1, v));
+                v1 = fmax(v1, v);
             }
         for (int off = 1; off < seg; off *= 2) {
-            const double oa = __shfl_xor(a, off, kWave), ob = __shfl_xor(b, off, kWave);
-            b = fmax(fmin(a, oa), fmax(b, ob));
-            a = fmax(a, oa);
+            const double o1 = __shfl_xor(v1, off, kWave), o2 = __shfl_xor(v2, off, kWave);
+            v2 = fmax(fmin(v1, o1), fmax(v2, o2));
+            v1 = fmax(v1, o1);
         }
-        if (g < c.n_groups && lane % seg == 0) gval[wave][g] = c.group_lead == 2 ? a + b : a;
+        if (g < c.n_groups && lane % seg == 0) gval[g] = c.group_lead == 2 ? v1 + v2 : v1;
         wave_lds_fence();
         bool open = false;
         if (lane < c.n_groups) {
-            const double mine = gval[wave][lane];
+            const double mine = gval[lane];
             int before = 0;
             for (int o = 0; o < c.n_groups; ++o) {
-                const double ov = gval[wave][o];
+                const double ov = gval[o];
                 before += (ov > mine || (ov == mine && o < lane)) ? 1 : 0;
             }
             open = before < c.topk_groups;
@@ -125,32 +147,50 @@ __global__ __launch_bounds__(kRouteThreads) void route_scored_kernel(const L *__
             const int e = i * kWave + lane;
             if (e < E && !((mask >> (e / gs)) & 1)) taken |= 1u << i;
         }
+        wave_lds_fence();  // the next token of this wave writes val again
     }
-    int mine = 0;          // lane j keeps pick j
-    bool shut = false;     // its key is -inf
-    for (int j = 0; j < c.topk; ++j) {
-        double bv = -INFINITY;
-        int bi = 0x7FFFFFFF;
+    // this lane's best open key, of equal ones the first; i = PER: none is open
+    double bv;
+    float bf;
+    int bi;
+    auto own_best = [&]() {
+        bv = -INFINITY;
+        bi = PER;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int e = i * kWave + lane;
-            const bool take = !((taken >> i) & 1u) && (key[i] > bv || (key[i] == bv && e < bi));
+            const bool take = !((taken >> i) & 1u) & ((bi == PER) | (key[i] > bv));
             bv = take ? key[i] : bv;
-            bi = take ? e : bi;
+            bi = take ? i : bi;
         }
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) {
-            const double ov = __shfl_xor(bv, off, kWave);
-            const int oi = __shfl_xor(bi, off, kWave);
-            const bool take = ov > bv || (ov == bv && oi < bi);
-            bv = take ? ov : bv;
-            bi = take ? oi : bi;
+        bf = (float)bv;
+    };
+    own_best();
+    int mine = 0;       // lane j keeps pick j
+    bool shut = false;  // its key is -inf
+    for (int j = 0; j < c.topk; ++j) {
+        const float m = wave_max(bf);
+        uint64_t same = __ballot(bi < PER && bf == m);
+        int l = __builtin_ctzll(same), id;
+        if ((same & (same - 1)) == 0) {
+            id = __builtin_amdgcn_readlane(bi, l) * kWave + l;
+        } else {
+            const double k0 = readlane64(bv, l);
+            const bool in = (same >> lane) & 1;
+            if (__ballot(in && bv != k0)) {  // the largest of the keys that round alike
+                double best = k0;
+                for (uint64_t r = same & (same - 1); r; r &= r - 1) best = fmax(best, readlane64(bv, __builtin_ctzll(r)));
+                same = __ballot(in && bv == best);
+            }
+            id = wave_min_int((same >> lane) & 1 ? bi * kWave + lane : 0x7FFFFFFF);
+            l = id & (kWave - 1);
         }
-        if ((bi & (kWave - 1)) == lane) taken |= 1u << ((bi / kWave) & 31);
+        const bool none = !(readlane64(bv, l) > -INFINITY);
         if (lane == j) {
-            mine = bi;
-            shut = !(bv > -INFINITY);
+            mine = id;
+            shut = none;
         }
+        if (lane == l) taken |= 1u << bi;
+        own_best();
     }
     const bool have = lane < c.topk;
     double s = have && !shut ? score(tame(logit_at(row, mine))) : 0.0;
@@ -159,67 +199,161 @@ __global__ __launch_bounds__(kRouteThreads) void route_scored_kernel(const L *__
         s = sum > 0.0 ? s / sum : 0.0;
     }
     if (have) {
-        ids[t * c.topk + lane] = mine;
-        w[t * c.topk + lane] = (float)(s * (double)c.scale);
+        ids[lane] = mine;
+        w[lane] = (float)(s * (double)c.scale);
     }
 }
 
-// Expert buckets: workgroup e counts the pairs of lower experts (its offset) and places its own
-// in increasing pair index.  Thread i owns the contiguous pairs [i C, (i + 1) C).
+template <int PER, typename L>
+__global__ __launch_bounds__(kRouteThreads) void route_scored_kernel(const L *__restrict__ logits, int64_t ldl,
+                                                                     const float *__restrict__ bias, int64_t T,
+                                                                     int32_t E, RouteCfg c, int32_t *__restrict__ ids,
+                                                                     float *__restrict__ w) {
+    __shared__ double val[kRouteWaves][PER * kWave];
+    __shared__ double gval[kRouteWaves][w4a8::kMaxRouteGroups];
+    const int wave = threadIdx.x >> 6;
+    const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
+    if (t >= T) return;  // whole waves; the LDS rows are each wave's own
+    route_scored_token<PER>(logits + t * ldl, bias, E, c, val[wave], gval[wave], ids + t * c.topk, w + t * c.topk);
+}
+
+// Expert buckets: a workgroup places the pairs of kPlaceE experts, in increasing pair index, behind
+// the pairs of all lower experts.  Wave w owns a contiguous run of pairs and reads it twice (once to
+// count, once to place), 64 pairs at a time: the ids come from L2, E / kPlaceE times over, which
+// for some 10^5 pairs costs less than a scan over chunks with its extra launches.
 // shared_T >= 0: a shared expert with that many slots follows.
-constexpr int kPlaceThreads = 256;
-__global__ __launch_bounds__(kPlaceThreads) void place_kernel(const int32_t *__restrict__ ids, int64_t P, int32_t E,
-                                                              int32_t k, int64_t shared_T,
-                                                              int32_t *__restrict__ offsets,
-                                                              int32_t *__restrict__ perm,
-                                                              int32_t *__restrict__ slot_row,
-                                                              int32_t *__restrict__ slot_of_pair) {
-    __shared__ int32_t sums[2][kPlaceThreads / kWave];
+constexpr int kPlaceE = 4;
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void place_kernel(const int32_t *__restrict__ ids, int64_t P, int32_t E,
+                                                        int32_t k, int64_t shared_T, int32_t *__restrict__ offsets,
+                                                        int32_t *__restrict__ perm, int32_t *__restrict__ slot_row,
+                                                        int32_t *__restrict__ slot_of_pair) {
+    constexpr int kWaves = THREADS / kWave, kDeep = 8;  // kDeep loads of 64 ids in flight
+    __shared__ int32_t below_s[kWaves], own_s[kPlaceE][kWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int32_t e = blockIdx.x;
-    const int64_t C = (P + kPlaceThreads - 1) / kPlaceThreads;
-    const int64_t p0 = tid * C < P ? tid * C : P, p1 = p0 + C < P ? p0 + C : P;
-    int32_t below = 0, own = 0;
-    for (int64_t p = p0; p < p1; ++p) {
-        const int32_t v = ids[p];
-        below += v < e ? 1 : 0;
-        own += v == e ? 1 : 0;
-    }
-    int32_t incl = own;
+    const int32_t e0 = blockIdx.x * kPlaceE;
+    const int64_t C = (P + kWaves * kWave - 1) / (kWaves * kWave) * kWave;  // whole chunks of 64 per wave
+    const int64_t p0 = wave * C, p1 = p0 + C < P ? p0 + C : P;
+    int32_t below = 0, own[kPlaceE] = {};
+    for (int64_t c = p0; c < p1; c += kDeep * kWave) {
+        int32_t v[kDeep];
 #pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) {
-        const int32_t o = __shfl_up(incl, off, kWave);
-        if (lane >= off) incl += o;
-    }
+        for (int j = 0; j < kDeep; ++j) {
+            const int64_t p = c + j * kWave + lane;
+            v[j] = p < p1 ? ids[p] : 0x7FFFFFFF;
+        }
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) below += __shfl_xor(below, off, kWave);
-    if (lane == kWave - 1) sums[0][wave] = incl;
-    if (lane == 0) sums[1][wave] = below;
+        for (int j = 0; j < kDeep; ++j) {
+            below += v[j] < e0 ? 1 : 0;
+#pragma unroll
+            for (int i = 0; i < kPlaceE; ++i) own[i] += v[j] == e0 + i ? 1 : 0;
+        }
+    }
+    auto wave_sum = [](int32_t v) {
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
+        return v;
+    };
+    below = wave_sum(below);
+#pragma unroll
+    for (int i = 0; i < kPlaceE; ++i) own[i] = wave_sum(own[i]);
+    if (lane == 0) {
+        below_s[wave] = below;
+#pragma unroll
+        for (int i = 0; i < kPlaceE; ++i) own_s[i][wave] = own[i];
+    }
     __syncthreads();
-    int32_t start = 0, before = 0, total = 0;
-    for (int i = 0; i < kPlaceThreads / kWave; ++i) {
-        start += sums[1][i];
-        total += sums[0][i];
-        if (i < wave) before += sums[0][i];
-    }
-    if (tid == 0) {
-        offsets[e] = start;
-        if (e == E - 1) {
-            offsets[E] = start + total;
-            if (shared_T >= 0) offsets[E + 1] = start + total + (int32_t)shared_T;
+    int32_t start = 0, slot[kPlaceE];  // slot: of this wave's next pair of each expert
+    for (int i = 0; i < kWaves; ++i) start += below_s[i];
+#pragma unroll
+    for (int i = 0; i < kPlaceE; ++i) {
+        if (e0 + i < E && tid == i) offsets[e0 + i] = start;
+        slot[i] = start;
+        for (int j = 0; j < kWaves; ++j) {
+            slot[i] += j < wave ? own_s[i][j] : 0;
+            start += own_s[i][j];
         }
     }
-    int32_t slot = start + before + incl - own;
-    for (int64_t p = p0; p < p1; ++p)
-        if (ids[p] == e) {
-            perm[slot] = (int32_t)p;
-            slot_of_pair[p] = slot;
-            if (slot_row) slot_row[slot] = (int32_t)(p / k);
-            ++slot;
+    if (e0 + kPlaceE >= E && tid == 0) {
+        offsets[E] = start;
+        if (shared_T >= 0) offsets[E + 1] = start + (int32_t)shared_T;
+    }
+    const uint64_t lt = (1ull << lane) - 1;
+    for (int64_t c = p0; c < p1; c += kDeep * kWave) {
+        int32_t v[kDeep];
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j) {
+            const int64_t p = c + j * kWave + lane;
+            v[j] = p < p1 ? ids[p] : 0x7FFFFFFF;
         }
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j) {
+            const int64_t p = c + j * kWave + lane;
+            if (!__ballot(v[j] >= e0 && v[j] < e0 + kPlaceE)) continue;
+#pragma unroll
+            for (int i = 0; i < kPlaceE; ++i) {
+                const uint64_t m = __ballot(v[j] == e0 + i);
+                if (v[j] == e0 + i) {
+                    const int32_t to = slot[i] + __popcll(m & lt);
+                    perm[to] = (int32_t)p;
+                    slot_of_pair[p] = to;
+                    if (slot_row) slot_row[to] = (int32_t)(p / k);
+                }
+                slot[i] += __popcll(m);
+            }
+        }
+    }
     if (slot_row)
-        for (int64_t t = (int64_t)e * kPlaceThreads + tid; t < shared_T; t += (int64_t)E * kPlaceThreads)
+        for (int64_t t = (int64_t)blockIdx.x * THREADS + tid; t < shared_T; t += (int64_t)gridDim.x * THREADS)
             slot_row[P + t] = (int32_t)t;
+}
+
+// Few tokens in one launch: one workgroup, a wave per token, then the buckets from the ids in LDS.
+// With so few pairs a slot is counted outright: pair p of expert e takes the number of pairs of
+// lower experts plus the number of earlier pairs of e.
+constexpr int kOneTokens = 16, kOneThreads = 64 * kOneTokens, kOnePairs = kOneTokens * w4a8::kMaxRouteK;
+template <int PER, typename L>
+__global__ __launch_bounds__(kOneThreads) void route_scored_one_kernel(
+    const L *__restrict__ logits, int64_t ldl, const float *__restrict__ bias, int32_t T, int32_t E, RouteCfg c,
+    int32_t shared_T, int32_t *__restrict__ ids, float *__restrict__ w, int32_t *__restrict__ offsets,
+    int32_t *__restrict__ perm, int32_t *__restrict__ slot_row, int32_t *__restrict__ slot_of_pair) {
+    __shared__ double val[kOneTokens][PER * kWave];
+    __shared__ double gval[kOneTokens][w4a8::kMaxRouteGroups];
+    __shared__ __attribute__((aligned(16))) int32_t all[kOnePairs];
+    __shared__ float all_w[kOnePairs];
+    const int tid = threadIdx.x, wave = tid >> 6;
+    const int P = T * c.topk;
+    for (int p = tid; p < (P + 3) / 4 * 4; p += kOneThreads) all[p] = 0x7FFFFFFF;  // whole reads of 4 below
+    __syncthreads();
+    if (wave < T)
+        route_scored_token<PER>(logits + wave * ldl, bias, E, c, val[wave], gval[wave], all + wave * c.topk,
+                                all_w + wave * c.topk);
+    __syncthreads();
+    // waves from the front take experts, from the back pairs
+    for (int e = tid; e <= E; e += kOneThreads) {
+        int32_t below = 0;
+        for (int q = 0; q < P; q += 4) {
+            const int4 v = *reinterpret_cast<const int4 *>(all + q);
+            below += (v.x < e ? 1 : 0) + (v.y < e ? 1 : 0) + (v.z < e ? 1 : 0) + (v.w < e ? 1 : 0);
+        }
+        offsets[e] = below;
+        if (e == E && shared_T >= 0) offsets[E + 1] = below + shared_T;
+    }
+    for (int p = kOneThreads - 1 - tid; p < P; p += kOneThreads) {
+        const int32_t e = all[p];
+        int32_t slot = 0;
+        for (int q = 0; q < P; q += 4) {
+            const int4 v = *reinterpret_cast<const int4 *>(all + q);
+            auto before = [&](int32_t o, int i) { return (o < e || (o == e && i < p)) ? 1 : 0; };
+            slot += before(v.x, q) + before(v.y, q + 1) + before(v.z, q + 2) + before(v.w, q + 3);
+        }
+        ids[p] = e;
+        w[p] = all_w[p];
+        perm[slot] = p;
+        slot_of_pair[p] = slot;
+        if (slot_row) slot_row[slot] = p / c.topk;
+    }
+    if (slot_row && tid < shared_T) slot_row[P + tid] = tid;
 }
 
 }  // namespace
@@ -227,15 +361,25 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(const int32_t *__r
 namespace w4a8 {
 
 template <typename L>
-static void route_typed(const L *logits, int64_t ldl, const float *bias, int64_t T, int32_t E, const RouteCfg &cfg,
-                        int32_t *ids, float *w, hipStream_t stream) {
+static void route_typed(const L *logits, int64_t ldl, const float *bias, int64_t T, int32_t E, int64_t shared_T,
+                        const RouteCfg &cfg, int32_t *ids, float *w, int32_t *offsets, int32_t *perm,
+                        int32_t *slot_row, int32_t *slot_of_pair, bool one, hipStream_t stream) {
     const dim3 grid((uint32_t)((T + kRouteWaves - 1) / kRouteWaves)), block(kRouteThreads);
     const int per = (E + kWave - 1) / kWave;
 #define W4A8_RS(PP)                                                                                                  \
-    hipLaunchKernelGGL((route_scored_kernel<PP, L>), grid, block, 0, stream, logits, ldl, bias, T, E, cfg, ids, w)
+    do {                                                                                                             \
+        if (one)                                                                                                     \
+            hipLaunchKernelGGL((route_scored_one_kernel<PP, L>), dim3(1), dim3(kOneThreads), 0, stream, logits, ldl, \
+                               bias, (int32_t)T, E, cfg, (int32_t)shared_T, ids, w, offsets, perm, slot_row,         \
+                               slot_of_pair);                                                                        \
+        else                                                                                                         \
+            hipLaunchKernelGGL((route_scored_kernel<PP, L>), grid, block, 0, stream, logits, ldl, bias, T, E, cfg,   \
+                               ids, w);                                                                              \
+    } while (0)
     if (per <= 1) W4A8_RS(1);
     else if (per <= 2) W4A8_RS(2);
     else if (per <= 4) W4A8_RS(4);
+    else if (per <= 6) W4A8_RS(6);
     else if (per <= 8) W4A8_RS(8);
     else W4A8_RS(16);
 #undef W4A8_RS
@@ -245,17 +389,25 @@ hipError_t launch_moe_route_scored(const void *logits, int32_t logits_type, int6
                                    int32_t E, int32_t with_shared, const RouteCfg &cfg, int32_t *ids, float *w,
                                    int32_t *offsets, int32_t *perm, int32_t *slot_row, int32_t *slot_of_pair,
                                    hipStream_t stream) {
+    const int64_t shared_T = with_shared ? T : (int64_t)-1, P = T * cfg.topk;
+    const bool one = T > 0 && T <= kOneTokens;
     if (T > 0) {
-        if (logits_type == W4A8_F16)
-            route_typed((const _Float16 *)logits, ldl, bias, T, E, cfg, ids, w, stream);
-        else if (logits_type == W4A8_BF16)
-            route_typed((const __bf16 *)logits, ldl, bias, T, E, cfg, ids, w, stream);
-        else
-            route_typed((const float *)logits, ldl, bias, T, E, cfg, ids, w, stream);
-        if (hipError_t err = hipGetLastError()) return err;
+#define W4A8_RT(L) \
+    route_typed((const L *)logits, ldl, bias, T, E, shared_T, cfg, ids, w, offsets, perm, slot_row, slot_of_pair, one, stream)
+        if (logits_type == W4A8_F16) W4A8_RT(_Float16);
+        else if (logits_type == W4A8_BF16) W4A8_RT(__bf16);
+        else W4A8_RT(float);
+#undef W4A8_RT
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess || one) return err;
     }
-    hipLaunchKernelGGL(place_kernel, dim3((uint32_t)E), dim3(kPlaceThreads), 0, stream, ids, T * cfg.topk, E, cfg.topk,
-                       with_shared ? T : (int64_t)-1, offsets, perm, slot_row, slot_of_pair);
+    const dim3 grid((uint32_t)((E + kPlaceE - 1) / kPlaceE));
+    if (P <= 2048)
+        hipLaunchKernelGGL(place_kernel<256>, grid, dim3(256), 0, stream, ids, P, E, cfg.topk, shared_T, offsets, perm,
+                           slot_row, slot_of_pair);
+    else
+        hipLaunchKernelGGL(place_kernel<1024>, grid, dim3(1024), 0, stream, ids, P, E, cfg.topk, shared_T, offsets,
+                           perm, slot_row, slot_of_pair);
     return hipGetLastError();
 }
 
