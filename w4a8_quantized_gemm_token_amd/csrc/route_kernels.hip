@@ -33,10 +33,25 @@ __device__ __forceinline__ float tame(float x) { return x > -INFINITY ? fminf(x,
 
 __device__ __forceinline__ double sigmoid64(float x) { return 1.0 / (1.0 + exp(-(double)x)); }
 
+__device__ __forceinline__ double readlane64(double v, int l) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)b, l), hi = __builtin_amdgcn_readlane((int)(b >> 32), l);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+// Sum over the wave, returned to every lane: DPP inside each 16-lane row, then the four rows.
+template <int CTRL>
+__device__ __forceinline__ double dpp_add64(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)b, CTRL, 0xF, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, 0xF, 0xF, false);
+    return v + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
 __device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
-    return v;
+    v = dpp_add64<0xB1>(v);   // quad_perm [1,0,3,2]
+    v = dpp_add64<0x4E>(v);   // quad_perm [2,3,0,1]
+    v = dpp_add64<0x124>(v);  // row_ror:4
+    v = dpp_add64<0x128>(v);  // row_ror:8
+    return (readlane64(v, 0) + readlane64(v, 16)) + (readlane64(v, 32) + readlane64(v, 48));
 }
 
 // Minimum over the wave, returned to every lane (DPP inside each 16-lane row, then the four rows).
@@ -52,12 +67,6 @@ __device__ __forceinline__ int wave_min_int(int v) {
     return min(min(__builtin_amdgcn_readlane(v, 0), __builtin_amdgcn_readlane(v, 16)),
                min(__builtin_amdgcn_readlane(v, 32), __builtin_amdgcn_readlane(v, 48)));
 }
-__device__ __forceinline__ double readlane64(double v, int l) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = __builtin_amdgcn_readlane((int)b, l), hi = __builtin_amdgcn_readlane((int)(b >> 32), l);
-    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
-}
-
 // Orders a wave's LDS writes before its other lanes' reads (LDS runs a wave's accesses in order;
 // this keeps the compiler from moving them).
 __device__ __forceinline__ void wave_lds_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
@@ -80,35 +89,38 @@ __device__ __forceinline__ void route_scored_token(const L *__restrict__ row, co
         b[i] = bias && e < E ? tame(bias[e]) : 0.0f;
     }
     const bool softmax = c.score == W4A8_SCORE_SOFTMAX;
-    double top = 0.0, denom = 1.0;
+    const bool scored = bias || c.n_groups > 1;  // else the logits themselves are the keys
+    double top = 0.0, inv = 1.0;
+    double key[PER];
     if (softmax) {
         float m = -INFINITY;
 #pragma unroll
         for (int i = 0; i < PER; ++i) m = fmaxf(m, x[i]);
         m = wave_max(m);
-        if (m > -INFINITY) {
-            top = (double)m;
-            double sum = 0.0;
+        top = m > -INFINITY ? (double)m : 0.0;  // no live logit: every exp is 0, and so is every score
+        double sum = 0.0;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) sum += exp((double)x[i] - top);
-            denom = wave_sum64(sum);
+        for (int i = 0; i < PER; ++i) {
+            key[i] = exp((double)x[i] - top);
+            sum += key[i];
         }
+        sum = wave_sum64(sum);
+        inv = sum > 0.0 ? 1.0 / sum : 0.0;
+    } else if (scored) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) key[i] = sigmoid64(x[i]);
     }
-    auto score = [&](float xv) -> double {
-        if (!(xv > -INFINITY)) return 0.0;
-        return softmax ? exp((double)xv - top) / denom : sigmoid64(xv);
-    };
-    const bool scored = bias || c.n_groups > 1;  // else the logits themselves are the keys
-    double key[PER];
     uint32_t taken = 0;  // bit i: expert i * 64 + lane is picked, outside E or in a closed group
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int e = i * kWave + lane;
-        if (e >= E) taken |= 1u << i;
-        double v = -INFINITY;
-        if (scored && x[i] > -INFINITY && b[i] > -INFINITY) v = score(x[i]) + (double)b[i];
-        if (c.n_groups > 1) val[i * kWave + lane] = v;
-        key[i] = bias ? v : (double)x[i];
+        if (i * kWave + lane >= E) taken |= 1u << i;
+        if (scored) {
+            const double v = x[i] > -INFINITY && b[i] > -INFINITY ? key[i] * inv + (double)b[i] : -INFINITY;
+            if (c.n_groups > 1) val[i * kWave + lane] = v;
+            key[i] = bias ? v : (double)x[i];
+        } else {
+            key[i] = (double)x[i];
+        }
     }
     if (c.n_groups > 1) {
         // 64 / n_groups lanes (a power of two) walk each group; their best two are merged
@@ -142,31 +154,35 @@ __device__ __forceinline__ void route_scored_token(const L *__restrict__ row, co
             open = before < c.topk_groups;
         }
         const uint64_t mask = __ballot(open);
+        // e / gs: (e + 1/2) / gs is 1 / (2 gs) from a whole number at least, far more than fp32 errs
+        const float per_gs = 1.0f / (float)gs;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int e = i * kWave + lane;
-            if (e < E && !((mask >> (e / gs)) & 1)) taken |= 1u << i;
+            if (e < E && !((mask >> (int)(((float)e + 0.5f) * per_gs)) & 1)) taken |= 1u << i;
         }
         wave_lds_fence();  // the next token of this wave writes val again
     }
     // this lane's best open key, of equal ones the first; i = PER: none is open
     double bv;
-    float bf;
+    float bf, bx;  // the key rounded, its logit
     int bi;
     auto own_best = [&]() {
         bv = -INFINITY;
+        bx = 0.0f;
         bi = PER;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const bool take = !((taken >> i) & 1u) & ((bi == PER) | (key[i] > bv));
             bv = take ? key[i] : bv;
+            bx = take ? x[i] : bx;
             bi = take ? i : bi;
         }
         bf = (float)bv;
     };
     own_best();
-    int mine = 0;       // lane j keeps pick j
-    bool shut = false;  // its key is -inf
+    int mine = 0;  // lane j keeps pick j, and its logit (-inf: weight 0)
+    float mine_x = -INFINITY;
     for (int j = 0; j < c.topk; ++j) {
         const float m = wave_max(bf);
         uint64_t same = __ballot(bi < PER && bf == m);
@@ -184,16 +200,18 @@ __device__ __forceinline__ void route_scored_token(const L *__restrict__ row, co
             id = wave_min_int((same >> lane) & 1 ? bi * kWave + lane : 0x7FFFFFFF);
             l = id & (kWave - 1);
         }
-        const bool none = !(readlane64(bv, l) > -INFINITY);
+        const float px = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, bx), l));
+        const bool shut = !(m > -INFINITY);  // a key of -inf
         if (lane == j) {
             mine = id;
-            shut = none;
+            mine_x = shut ? -INFINITY : px;
         }
         if (lane == l) taken |= 1u << bi;
         own_best();
     }
     const bool have = lane < c.topk;
-    double s = have && !shut ? score(tame(logit_at(row, mine))) : 0.0;
+    // (exp(-inf) is 0: a lane without a pick, or with a masked one, has score 0)
+    double s = softmax ? exp((double)mine_x - top) * inv : sigmoid64(mine_x);
     if (c.renorm) {
         const double sum = wave_sum64(s);
         s = sum > 0.0 ? s / sum : 0.0;
@@ -217,94 +235,110 @@ __global__ __launch_bounds__(kRouteThreads) void route_scored_kernel(const L *__
     route_scored_token<PER>(logits + t * ldl, bias, E, c, val[wave], gval[wave], ids + t * c.topk, w + t * c.topk);
 }
 
-// Expert buckets: a workgroup places the pairs of kPlaceE experts, in increasing pair index, behind
-// the pairs of all lower experts.  Wave w owns a contiguous run of pairs and reads it twice (once to
-// count, once to place), 64 pairs at a time: the ids come from L2, E / kPlaceE times over, which
-// for some 10^5 pairs costs less than a scan over chunks with its extra launches.
+// Expert buckets: workgroup e places the pairs of expert e, in increasing pair index, behind the
+// pairs of all lower experts.  Each wave owns a contiguous run of pairs and reads it twice (to count,
+// then to place), 256 pairs at a time, four neighbours per lane, counting with ballots.  The ids
+// come from L2, E times over, which for some 10^5 pairs costs less than a scan over chunks with
+// its extra launches.
 // shared_T >= 0: a shared expert with that many slots follows.
-constexpr int kPlaceE = 4;
+typedef int32_t ids4 __attribute__((ext_vector_type(4), aligned(4)));
 template <int THREADS>
-__global__ __launch_bounds__(THREADS) void place_kernel(const int32_t *__restrict__ ids, int64_t P, int32_t E,
-                                                        int32_t k, int64_t shared_T, int32_t *__restrict__ offsets,
+__global__ __launch_bounds__(THREADS) void place_kernel(const int32_t *__restrict__ ids, int32_t P, int32_t E,
+                                                        int32_t k, int32_t shared_T, int32_t *__restrict__ offsets,
                                                         int32_t *__restrict__ perm, int32_t *__restrict__ slot_row,
                                                         int32_t *__restrict__ slot_of_pair) {
-    constexpr int kWaves = THREADS / kWave, kDeep = 8;  // kDeep loads of 64 ids in flight
-    __shared__ int32_t below_s[kWaves], own_s[kPlaceE][kWaves];
+    constexpr int kWaves = THREADS / kWave, kChunk = 4 * kWave, kList = 8 * THREADS;
+    __shared__ int32_t below_s[kWaves], own_s[kWaves], list[kList];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int32_t e0 = blockIdx.x * kPlaceE;
-    const int64_t C = (P + kWaves * kWave - 1) / (kWaves * kWave) * kWave;  // whole chunks of 64 per wave
-    const int64_t p0 = wave * C, p1 = p0 + C < P ? p0 + C : P;
-    int32_t below = 0, own[kPlaceE] = {};
-    for (int64_t c = p0; c < p1; c += kDeep * kWave) {
-        int32_t v[kDeep];
+    const int32_t e = blockIdx.x;
+    const int64_t chunks = ((int64_t)P + kChunk - 1) / kChunk;
+    const int64_t p0 = chunks * wave / kWaves * kChunk, p1 = chunks * (wave + 1) / kWaves * kChunk;
+    // calls f(c, ids of the pairs c + 4 lane + 0..3) for the wave's chunks, with kDeep chunks' loads in
+    // flight (their latency is most of the time); past the end the ids are above all
+    constexpr int kDeep = 8;
+    auto walk = [&](auto f) {
+        for (int64_t c = p0; c < p1; c += kDeep * kChunk) {
+            ids4 v[kDeep];
+            if (c + kDeep * kChunk <= p1 && c + kDeep * kChunk <= P) {
 #pragma unroll
-        for (int j = 0; j < kDeep; ++j) {
-            const int64_t p = c + j * kWave + lane;
-            v[j] = p < p1 ? ids[p] : 0x7FFFFFFF;
-        }
+                for (int d = 0; d < kDeep; ++d) v[d] = *reinterpret_cast<const ids4 *>(ids + c + d * kChunk + 4 * lane);
 #pragma unroll
-        for (int j = 0; j < kDeep; ++j) {
-            below += v[j] < e0 ? 1 : 0;
+                for (int d = 0; d < kDeep; ++d) f(c + d * kChunk, v[d]);
+            } else {
+                for (int64_t c1 = c; c1 < p1; c1 += kChunk) {
 #pragma unroll
-            for (int i = 0; i < kPlaceE; ++i) own[i] += v[j] == e0 + i ? 1 : 0;
-        }
-    }
-    auto wave_sum = [](int32_t v) {
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
-        return v;
-    };
-    below = wave_sum(below);
-#pragma unroll
-    for (int i = 0; i < kPlaceE; ++i) own[i] = wave_sum(own[i]);
-    if (lane == 0) {
-        below_s[wave] = below;
-#pragma unroll
-        for (int i = 0; i < kPlaceE; ++i) own_s[i][wave] = own[i];
-    }
-    __syncthreads();
-    int32_t start = 0, slot[kPlaceE];  // slot: of this wave's next pair of each expert
-    for (int i = 0; i < kWaves; ++i) start += below_s[i];
-#pragma unroll
-    for (int i = 0; i < kPlaceE; ++i) {
-        if (e0 + i < E && tid == i) offsets[e0 + i] = start;
-        slot[i] = start;
-        for (int j = 0; j < kWaves; ++j) {
-            slot[i] += j < wave ? own_s[i][j] : 0;
-            start += own_s[i][j];
-        }
-    }
-    if (e0 + kPlaceE >= E && tid == 0) {
-        offsets[E] = start;
-        if (shared_T >= 0) offsets[E + 1] = start + (int32_t)shared_T;
-    }
-    const uint64_t lt = (1ull << lane) - 1;
-    for (int64_t c = p0; c < p1; c += kDeep * kWave) {
-        int32_t v[kDeep];
-#pragma unroll
-        for (int j = 0; j < kDeep; ++j) {
-            const int64_t p = c + j * kWave + lane;
-            v[j] = p < p1 ? ids[p] : 0x7FFFFFFF;
-        }
-#pragma unroll
-        for (int j = 0; j < kDeep; ++j) {
-            const int64_t p = c + j * kWave + lane;
-            if (!__ballot(v[j] >= e0 && v[j] < e0 + kPlaceE)) continue;
-#pragma unroll
-            for (int i = 0; i < kPlaceE; ++i) {
-                const uint64_t m = __ballot(v[j] == e0 + i);
-                if (v[j] == e0 + i) {
-                    const int32_t to = slot[i] + __popcll(m & lt);
-                    perm[to] = (int32_t)p;
-                    slot_of_pair[p] = to;
-                    if (slot_row) slot_row[to] = (int32_t)(p / k);
+                    for (int j = 0; j < 4; ++j) {
+                        const int64_t p = c1 + 4 * lane + j;
+                        const int32_t id = ids[p < P ? p : P - 1];
+                        v[0][j] = p < P ? id : 0x7FFFFFFF;
+                    }
+                    f(c1, v[0]);
                 }
-                slot[i] += __popcll(m);
             }
         }
+    };
+    int32_t below = 0, own = 0;
+    walk([&](int64_t, const ids4 &v) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            below += __popcll(__ballot(v[j] < e));
+            own += __popcll(__ballot(v[j] == e));
+        }
+    });
+    if (lane == 0) {
+        below_s[wave] = below;
+        own_s[wave] = own;
+    }
+    __syncthreads();
+    int32_t start = 0, before = 0, total = 0;  // before: the expert's pairs in earlier waves' runs
+    for (int i = 0; i < kWaves; ++i) {
+        start += below_s[i];
+        before += i < wave ? own_s[i] : 0;
+        total += own_s[i];
+    }
+    if (tid == 0) {
+        offsets[e] = start;
+        if (e == E - 1) {
+            offsets[E] = start + total;
+            if (shared_T >= 0) offsets[E + 1] = start + total + shared_T;
+        }
+    }
+    // The expert's pairs go through a list in LDS, kList of them a round, so that the scattered
+    // writes and the division are made by full waves, not by the one lane in 64 that found a pair.
+    const uint64_t lt = (1ull << lane) - 1;
+    for (int32_t base = 0; base < total; base += kList) {
+        int32_t next = before - base;  // list place of this wave's next pair
+        if (own > 0)
+            walk([&](int64_t c, const ids4 &v) {
+                uint64_t m[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m[j] = __ballot(v[j] == e);
+                if (!(m[0] | m[1] | m[2] | m[3])) return;
+                int32_t to = next;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    to += __popcll(m[j] & lt);
+                    next += __popcll(m[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (v[j] == e) {
+                        if (to >= 0 && to < kList) list[to] = (int32_t)(c + 4 * lane + j);
+                        ++to;
+                    }
+            });
+        __syncthreads();
+        const int32_t n = total - base < kList ? total - base : kList;
+        for (int32_t i = tid; i < n; i += THREADS) {
+            const int32_t p = list[i], slot = start + base + i;
+            perm[slot] = p;
+            slot_of_pair[p] = slot;
+            if (slot_row) slot_row[slot] = p / k;
+        }
+        __syncthreads();
     }
     if (slot_row)
-        for (int64_t t = (int64_t)blockIdx.x * THREADS + tid; t < shared_T; t += (int64_t)gridDim.x * THREADS)
+        for (int64_t t = (int64_t)e * THREADS + tid; t < shared_T; t += (int64_t)E * THREADS)
             slot_row[P + t] = (int32_t)t;
 }
 
@@ -401,13 +435,12 @@ hipError_t launch_moe_route_scored(const void *logits, int32_t logits_type, int6
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess || one) return err;
     }
-    const dim3 grid((uint32_t)((E + kPlaceE - 1) / kPlaceE));
     if (P <= 2048)
-        hipLaunchKernelGGL(place_kernel<256>, grid, dim3(256), 0, stream, ids, P, E, cfg.topk, shared_T, offsets, perm,
-                           slot_row, slot_of_pair);
+        hipLaunchKernelGGL((place_kernel<256>), dim3((uint32_t)E), dim3(256), 0, stream, ids, (int32_t)P, E, cfg.topk,
+                           (int32_t)shared_T, offsets, perm, slot_row, slot_of_pair);
     else
-        hipLaunchKernelGGL(place_kernel<1024>, grid, dim3(1024), 0, stream, ids, P, E, cfg.topk, shared_T, offsets,
-                           perm, slot_row, slot_of_pair);
+        hipLaunchKernelGGL((place_kernel<1024>), dim3((uint32_t)E), dim3(1024), 0, stream, ids, (int32_t)P, E, cfg.topk,
+                           (int32_t)shared_T, offsets, perm, slot_row, slot_of_pair);
     return hipGetLastError();
 }
 
