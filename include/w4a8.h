@@ -330,8 +330,9 @@ w4a8_status w4a8_moe_route(const float *logits, int64_t T, int32_t E, int32_t to
 /* Device.  Router by scores, for models whose picks are not the plain top-k of the
  * logits; it writes the same tables as w4a8_moe_route.  With x = logits[t][e] (NaN
  * counts as -inf, values above the largest fp32 as that):
- *   s   = 1 / (1 + exp(-x)) (score W4A8_SCORE_SIGMOID) or the softmax of the token's
- *         logits (W4A8_SCORE_SOFTMAX); 0 where x is -inf
+ *   s   = 1 / (1 + exp(-x)) (score W4A8_SCORE_SIGMOID; 0 for x below -708, where
+ *         fp64 ends) or the softmax of the token's logits (W4A8_SCORE_SOFTMAX); 0
+ *         where x is -inf
  *   v   = s + bias[e], or s without a bias; the picks' order goes by key = v, or by x
  *         itself without a bias.  bias: fp32 [E] or NULL, NaN counting as -inf.  An
  *         expert whose logit or bias is -inf has v = key = -inf

@@ -31,7 +31,43 @@ __device__ __forceinline__ float logit_at(const __bf16 *p, int64_t i) { return (
 // NaN -> -inf (no comparison with it holds), +inf -> the largest fp32
 __device__ __forceinline__ float tame(float x) { return x > -INFINITY ? fminf(x, 3.402823466e38f) : -INFINITY; }
 
-__device__ __forceinline__ double sigmoid64(float x) { return 1.0 / (1.0 + exp(-(double)x)); }
+// e^d for d <= 709 (-inf: 0) in fp64: d = n ln 2 + r with |r| <= ln 2 / 2, the Taylor series of e^r to
+// r^13 (the rest is below 2^-59) and a scaling by 2^n.  About 20 instructions, where the library's
+// form with its special cases takes some 40, and a token needs one for each expert.
+__device__ __forceinline__ double exp64(double d) {
+    d = fmax(d, -1100.0);  // 2^-1587 and below: 0
+    const double n = __builtin_rint(d * 1.4426950408889634);
+    // ln 2 in two parts, the first with 21 trailing zero bits: n times it is exact
+    const double r = fma(n, -1.9082149292705877e-10, fma(n, -0.693147180369123816490, d));
+    double p = 1.0 / 6227020800.0;
+    p = fma(p, r, 1.0 / 479001600.0);
+    p = fma(p, r, 1.0 / 39916800.0);
+    p = fma(p, r, 1.0 / 3628800.0);
+    p = fma(p, r, 1.0 / 362880.0);
+    p = fma(p, r, 1.0 / 40320.0);
+    p = fma(p, r, 1.0 / 5040.0);
+    p = fma(p, r, 1.0 / 720.0);
+    p = fma(p, r, 1.0 / 120.0);
+    p = fma(p, r, 1.0 / 24.0);
+    p = fma(p, r, 1.0 / 6.0);
+    p = fma(p, r, 0.5);
+    p = fma(p, r, 1.0);
+    p = fma(p, r, 1.0);
+    return __builtin_ldexp(p, (int)n);
+}
+
+// 1 / a for 1 <= a < 2^1023: the hardware's approximate reciprocal and two Newton steps
+__device__ __forceinline__ double recip64(double a) {
+    double y = __builtin_amdgcn_rcp(a);
+    y = fma(fma(-a, y, 1.0), y, y);
+    return fma(fma(-a, y, 1.0), y, y);
+}
+
+// (e^708 is the last whole power that fp64 holds with room to spare: below -708 the score is 0)
+__device__ __forceinline__ double sigmoid64(float x) {
+    const double s = recip64(1.0 + exp64(fmin(-(double)x, 708.0)));
+    return x < -708.0f ? 0.0 : s;
+}
 
 __device__ __forceinline__ double readlane64(double v, int l) {
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
@@ -54,27 +90,28 @@ __device__ __forceinline__ double wave_sum64(double v) {
     return (readlane64(v, 0) + readlane64(v, 16)) + (readlane64(v, 32) + readlane64(v, 48));
 }
 
-// Minimum over the wave, returned to every lane (DPP inside each 16-lane row, then the four rows).
+// Maximum over the wave, returned to every lane.
 template <int CTRL>
-__device__ __forceinline__ int dpp_min(int v) {
-    return min(v, __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false));
+__device__ __forceinline__ int dpp_max_int(int v) {
+    return max(v, __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false));
 }
-__device__ __forceinline__ int wave_min_int(int v) {
-    v = dpp_min<0xB1>(v);   // quad_perm [1,0,3,2]
-    v = dpp_min<0x4E>(v);   // quad_perm [2,3,0,1]
-    v = dpp_min<0x124>(v);  // row_ror:4
-    v = dpp_min<0x128>(v);  // row_ror:8
-    return min(min(__builtin_amdgcn_readlane(v, 0), __builtin_amdgcn_readlane(v, 16)),
-               min(__builtin_amdgcn_readlane(v, 32), __builtin_amdgcn_readlane(v, 48)));
+__device__ __forceinline__ int wave_max_int(int v) {
+    v = dpp_max_int<0xB1>(v);   // quad_perm [1,0,3,2]
+    v = dpp_max_int<0x4E>(v);   // quad_perm [2,3,0,1]
+    v = dpp_max_int<0x124>(v);  // row_ror:4
+    v = dpp_max_int<0x128>(v);  // row_ror:8
+    return max(max(__builtin_amdgcn_readlane(v, 0), __builtin_amdgcn_readlane(v, 16)),
+               max(__builtin_amdgcn_readlane(v, 32), __builtin_amdgcn_readlane(v, 48)));
 }
+
 // Orders a wave's LDS writes before its other lanes' reads (LDS runs a wave's accesses in order;
 // this keeps the compiler from moving them).
 __device__ __forceinline__ void wave_lds_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
 // Routes one token with one wave; lane l holds experts l, l + 64, ... (PER of them).
-// A pick is the wave's largest key: each lane keeps its own best open key in fp64 and that rounded
-// to fp32; the rounding keeps the order, so the fp32 maximum (a few DPP steps) names the winner
-// unless several lanes share it, and only those are then compared in fp64, and by id.
+// The picks go by the keys rounded to fp32, as integers of the same order (the rounding keeps the
+// order of the keys): a pick is the wave's maximum, a few DPP steps, and nearly always one expert
+// has it.  Where several do, their fp64 keys decide, and then the lower id.
 // val, gval: the wave's own LDS, used when there are groups.
 template <int PER, typename L>
 __device__ __forceinline__ void route_scored_token(const L *__restrict__ row, const float *__restrict__ bias, int32_t E,
@@ -101,7 +138,7 @@ __device__ __forceinline__ void route_scored_token(const L *__restrict__ row, co
         double sum = 0.0;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            key[i] = exp((double)x[i] - top);
+            key[i] = exp64((double)x[i] - top);
             sum += key[i];
         }
         sum = wave_sum64(sum);
@@ -110,10 +147,10 @@ __device__ __forceinline__ void route_scored_token(const L *__restrict__ row, co
 #pragma unroll
         for (int i = 0; i < PER; ++i) key[i] = sigmoid64(x[i]);
     }
-    uint32_t taken = 0;  // bit i: expert i * 64 + lane is picked, outside E or in a closed group
+    constexpr int kClosed = -0x7FFFFFFF - 1;  // picked, outside E or in a closed group (-inf is above it)
+    int ord[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        if (i * kWave + lane >= E) taken |= 1u << i;
         if (scored) {
             const double v = x[i] > -INFINITY && b[i] > -INFINITY ? key[i] * inv + (double)b[i] : -INFINITY;
             if (c.n_groups > 1) val[i * kWave + lane] = v;
@@ -121,6 +158,8 @@ __device__ __forceinline__ void route_scored_token(const L *__restrict__ row, co
         } else {
             key[i] = (double)x[i];
         }
+        const int f = __builtin_bit_cast(int, (float)key[i] + 0.0f);  // (-0 as 0)
+        ord[i] = i * kWave + lane < E ? f ^ ((f >> 31) & 0x7FFFFFFF) : kClosed;
     }
     if (c.n_groups > 1) {
         // 64 / n_groups lanes (a power of two) walk each group; their best two are merged
@@ -159,59 +198,62 @@ __device__ __forceinline__ void route_scored_token(const L *__restrict__ row, co
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int e = i * kWave + lane;
-            if (e < E && !((mask >> (int)(((float)e + 0.5f) * per_gs)) & 1)) taken |= 1u << i;
+            if (e < E && !((mask >> (int)(((float)e + 0.5f) * per_gs)) & 1)) ord[i] = kClosed;
         }
         wave_lds_fence();  // the next token of this wave writes val again
     }
-    // this lane's best open key, of equal ones the first; i = PER: none is open
-    double bv;
-    float bf, bx;  // the key rounded, its logit
-    int bi;
-    auto own_best = [&]() {
-        bv = -INFINITY;
-        bx = 0.0f;
-        bi = PER;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const bool take = !((taken >> i) & 1u) & ((bi == PER) | (key[i] > bv));
-            bv = take ? key[i] : bv;
-            bx = take ? x[i] : bx;
-            bi = take ? i : bi;
-        }
-        bf = (float)bv;
-    };
-    own_best();
+    constexpr int kOrdInf = (int)0xFF800000 ^ 0x7FFFFFFF;  // the order of -inf
     int mine = 0;  // lane j keeps pick j, and its logit (-inf: weight 0)
     float mine_x = -INFINITY;
     for (int j = 0; j < c.topk; ++j) {
-        const float m = wave_max(bf);
-        uint64_t same = __ballot(bi < PER && bf == m);
-        int l = __builtin_ctzll(same), id;
-        if ((same & (same - 1)) == 0) {
-            id = __builtin_amdgcn_readlane(bi, l) * kWave + l;
-        } else {
-            const double k0 = readlane64(bv, l);
-            const bool in = (same >> lane) & 1;
-            if (__ballot(in && bv != k0)) {  // the largest of the keys that round alike
-                double best = k0;
-                for (uint64_t r = same & (same - 1); r; r &= r - 1) best = fmax(best, readlane64(bv, __builtin_ctzll(r)));
-                same = __ballot(in && bv == best);
-            }
-            id = wave_min_int((same >> lane) & 1 ? bi * kWave + lane : 0x7FFFFFFF);
-            l = id & (kWave - 1);
+        int m = ord[0];
+#pragma unroll
+        for (int i = 1; i < PER; ++i) m = max(m, ord[i]);
+        m = wave_max_int(m);
+        int count = 0, id = 0;
+#pragma unroll
+        for (int i = PER - 1; i >= 0; --i) {  // the lowest id with the maximum, and how many have it
+            const uint64_t same = __ballot(ord[i] == m);
+            count += __popcll(same);
+            if (same) id = i * kWave + __builtin_ctzll(same);
         }
-        const float px = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, bx), l));
-        const bool shut = !(m > -INFINITY);  // a key of -inf
+        if (count > 1) {
+            double best = 0.0;
+            bool first = true;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                uint64_t same = __ballot(ord[i] == m);
+                if (!same) continue;
+                if (first) {
+                    best = readlane64(key[i], __builtin_ctzll(same));
+                    first = false;
+                }
+                // the lanes whose key is above the best so far, in turn (equal ones: none)
+                for (uint64_t up = __ballot(ord[i] == m && key[i] > best); up;
+                     up = __ballot(ord[i] == m && key[i] > best)) {
+                    const int l = __builtin_ctzll(up);
+                    best = readlane64(key[i], l);
+                    id = i * kWave + l;
+                }
+            }
+        }
+        const int l = id & (kWave - 1);
+        float px = 0.0f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (id / kWave == i) {
+                px = x[i];
+                if (lane == l) ord[i] = kClosed;
+            }
+        px = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, px), l));
         if (lane == j) {
             mine = id;
-            mine_x = shut ? -INFINITY : px;
+            mine_x = m == kOrdInf ? -INFINITY : px;  // a key of -inf: no weight
         }
-        if (lane == l) taken |= 1u << bi;
-        own_best();
     }
     const bool have = lane < c.topk;
-    // (exp(-inf) is 0: a lane without a pick, or with a masked one, has score 0)
-    double s = softmax ? exp((double)mine_x - top) * inv : sigmoid64(mine_x);
+    // a lane without a pick, or with a masked one, has score 0
+    double s = softmax ? exp64((double)mine_x - top) * inv : sigmoid64(mine_x);  // -inf: 0
     if (c.renorm) {
         const double sum = wave_sum64(s);
         s = sum > 0.0 ? s / sum : 0.0;
@@ -412,6 +454,7 @@ static void route_typed(const L *logits, int64_t ldl, const float *bias, int64_t
     } while (0)
     if (per <= 1) W4A8_RS(1);
     else if (per <= 2) W4A8_RS(2);
+    else if (per <= 3) W4A8_RS(3);
     else if (per <= 4) W4A8_RS(4);
     else if (per <= 6) W4A8_RS(6);
     else if (per <= 8) W4A8_RS(8);
