@@ -14,6 +14,8 @@
 // An expert whose logit or bias is -inf has v = key = -inf and weight 0.  Scores and keys are
 // held in fp64: two experts' keys often differ by less than an fp32 ulp, and the picks
 // should be those of the formula.
+#include <type_traits>
+
 #include "w8_internal.hpp"
 
 using namespace w4a8dev;
@@ -295,28 +297,32 @@ __global__ __launch_bounds__(THREADS) void place_kernel(const int32_t *__restric
     const int32_t e = blockIdx.x;
     const int64_t chunks = ((int64_t)P + kChunk - 1) / kChunk;
     const int64_t p0 = chunks * wave / kWaves * kChunk, p1 = chunks * (wave + 1) / kWaves * kChunk;
-    // calls f(c, ids of the pairs c + 4 lane + 0..3) for the wave's chunks, with kDeep chunks' loads in
-    // flight (their latency is most of the time); past the end the ids are above all
-    constexpr int kDeep = 8;
+    // calls f(c, ids of the pairs c + 4 lane + 0..3) for the wave's chunks, with the loads of 8 or 2 of
+    // them in flight (their latency is most of the time); past the end the ids are above all
     auto walk = [&](auto f) {
-        for (int64_t c = p0; c < p1; c += kDeep * kChunk) {
-            ids4 v[kDeep];
-            if (c + kDeep * kChunk <= p1 && c + kDeep * kChunk <= P) {
+        const int64_t whole = p1 < P ? p1 : P;
+        int64_t c = p0;
+        auto batch = [&](auto deep) {
+            constexpr int D = decltype(deep)::value;
+            for (; c + D * kChunk <= whole; c += D * kChunk) {
+                ids4 v[D];
 #pragma unroll
-                for (int d = 0; d < kDeep; ++d) v[d] = *reinterpret_cast<const ids4 *>(ids + c + d * kChunk + 4 * lane);
+                for (int d = 0; d < D; ++d) v[d] = *reinterpret_cast<const ids4 *>(ids + c + d * kChunk + 4 * lane);
 #pragma unroll
-                for (int d = 0; d < kDeep; ++d) f(c + d * kChunk, v[d]);
-            } else {
-                for (int64_t c1 = c; c1 < p1; c1 += kChunk) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int64_t p = c1 + 4 * lane + j;
-                        const int32_t id = ids[p < P ? p : P - 1];
-                        v[0][j] = p < P ? id : 0x7FFFFFFF;
-                    }
-                    f(c1, v[0]);
-                }
+                for (int d = 0; d < D; ++d) f(c + d * kChunk, v[d]);
             }
+        };
+        batch(std::integral_constant<int, 8>{});
+        batch(std::integral_constant<int, 2>{});
+        for (; c < p1; c += kChunk) {
+            ids4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t p = c + 4 * lane + j;
+                const int32_t id = ids[p < P ? p : P - 1];
+                v[j] = p < P ? id : 0x7FFFFFFF;
+            }
+            f(c, v);
         }
     };
     int32_t below = 0, own = 0;
