@@ -160,6 +160,13 @@ def test_no_tokens():
         assert to_host(got[2]).tolist() == [0] * (13 + shared)
 
 
+@pytest.mark.parametrize("T", [17, 700, 9001, 20011])
+def test_every_token_picks_the_same_experts(T):
+    """All pairs in k buckets (longer than a workgroup's list), the others empty."""
+    x = np.tile(logits_of(8, 1, 40), (T, 1))
+    run(x, 3, score="sigmoid", with_shared=True)
+
+
 @pytest.mark.parametrize("T,E,k", [(20011, 160, 6), (9000, 384, 8)])
 def test_long_batches(T, E, k):
     """Many chunks of pairs: the tables against stable sorting, the picks against the fp64 keys' order."""

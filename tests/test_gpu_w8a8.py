@@ -74,6 +74,31 @@ def test_dense_types_bias_strides(dtype, bias, M, K, N, ldo):
     dense(np.random.default_rng(M + K), M, K, N, bias, dtype, ldo)
 
 
+# column counts at which each loop is taken: k shared out within a workgroup (up to 16 rows), and the tiles of 64 x 64,
+# 128 x 128, 128 x 256 and 256 x 256 (the sizes above take 32 x 64)
+LOOPS = [(1, 16400), (13, 16400), (16, 28677), (100, 8330), (130, 14341), (130, 28677), (257, 28677), (300, 57001)]
+
+
+@pytest.mark.parametrize("M,N", LOOPS)
+@pytest.mark.parametrize("K", [16, 128, 144, 400, 1040])
+def test_dense_loops(M, N, K):
+    dense(np.random.default_rng(M + N + K), M, K, N, bias=K % 3 == 0, dtype="f16" if K == 400 else "f32")
+
+
+@pytest.mark.parametrize("M,N", LOOPS)
+def test_dense_loops_strided_and_bf16(M, N):
+    """Row strides that keep the stores 16-byte aligned, and that do not."""
+    for ldo in (N + 8 - N % 8, N + 3):
+        dense(np.random.default_rng(M + ldo), M, 272, N, True, "bf16", ldo)
+
+
+@pytest.mark.parametrize("M", [1, 7, 16])
+@pytest.mark.parametrize("K", [2048, 7168, 8192, 8208, 8320, 16384, 24592])
+def test_dense_shared_k(M, K):
+    """Few rows, k in one and in several passes over it, with and without a part window."""
+    dense(np.random.default_rng(K + M), M, K, 16390 if K <= 8192 else 50, M == 7, "f32")
+
+
 @pytest.mark.parametrize("M,K,N", [(1, 8192, 4100), (16, 8192, 2048), (77, 4112, 5003), (512, 4096, 1040),
                                    (1, 131056, 48), (33, 131056, 80), (1000, 1040, 3001)])
 def test_dense_larger(M, K, N):
@@ -119,12 +144,12 @@ def test_rows_do_not_depend_on_the_batch():
     """A row gives the same bytes alone and in every batch size (every loop)."""
     w4 = w4mod()
     rng = np.random.default_rng(3)
-    M, K, N = 300, 1168, 520
-    qa, qw, sa, sw = (to_dev(v) for v in (codes(rng, M, K), codes(rng, N, K), scales(rng, M), scales(rng, N)))
-    whole = w4.gemm_w8a8(qa, sa, qw, sw)
-    for m in (1, 16, 17, 40, 64, 100, 129, 256):
-        part = w4.gemm_w8a8(qa[:m], sa[:m], qw, sw)
-        assert torch.equal(part.view(torch.int32), whole[:m].view(torch.int32)), m
+    for M, K, N in ((300, 1168, 520), (300, 144, 28700), (120, 528, 8330)):
+        qa, qw, sa, sw = (to_dev(v) for v in (codes(rng, M, K), codes(rng, N, K), scales(rng, M), scales(rng, N)))
+        whole = w4.gemm_w8a8(qa, sa, qw, sw)
+        for m in (1, 16, 17, 40, 64, 100, 129, 256):
+            part = w4.gemm_w8a8(qa[:m], sa[:m], qw, sw)
+            assert torch.equal(part.view(torch.int32), whole[:m].view(torch.int32)), (N, m)
 
 
 def test_weights_from_the_row_quantizer():
@@ -175,6 +200,18 @@ def grouped(rng, counts, K, N, R=None, rows="random", pad=0, repeat=False):
 @pytest.mark.parametrize("K,N", [(16, 5), (400, 132), (1040, 257)])
 def test_grouped_sizes(counts, K, N):
     grouped(np.random.default_rng(sum(counts) + N), counts, K, N)
+
+
+@pytest.mark.parametrize("K", [128, 2048, 3600, 7168, 8208, 16512])
+def test_grouped_few_slots(K):
+    """Up to 16 slots each: k in one and in several passes; more tiles than workgroups, so that runs cross experts."""
+    grouped(np.random.default_rng(K), [1, 16, 0, 3, 9, 2, 16, 1], K, 1552)
+
+
+@pytest.mark.parametrize("counts,K,N", [([17, 300, 0, 129, 64], 2064, 520), ([40] * 30, 144, 2570), ([1000, 3, 20], 656, 300)])
+def test_grouped_more_slots(counts, K, N):
+    """Row blocks of 128, several of an expert, more units than workgroups."""
+    grouped(np.random.default_rng(K), counts, K, N)
 
 
 @pytest.mark.parametrize("rows", [None, "random", "outside"])
