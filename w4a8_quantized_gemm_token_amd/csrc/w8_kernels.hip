@@ -74,7 +74,7 @@ struct Tile {
 };
 
 // src_row(r), r < rows: activation row of the tile's row r, or -1 (computed as row 0, not stored).
-// vec: output rows start 16-byte aligned.  WIDE: rows may lie 2^32 bytes or more behind qa.  (Its
+// WIDE: rows may lie 2^32 bytes or more behind qa.  (Its
 // loads take 64-bit addresses, and the compiler counts those as able to touch LDS by themselves:
 // it then waits for every access in flight where it would wait for some.)
 template <typename C, bool WIDE, typename T, typename SrcRow>
@@ -82,7 +82,7 @@ __device__ __forceinline__ void tile_unit(uint8_t *lds, const int8_t *__restrict
                                           const float *__restrict__ a_scale, SrcRow src_row, int64_t slot0, int rows,
                                           int64_t K, const int8_t *__restrict__ qw,
                                           const float *__restrict__ w_scale, int64_t N, int64_t n0,
-                                          const float *__restrict__ bias, T *__restrict__ out, int64_t ldo, bool vec) {
+                                          const float *__restrict__ bias, T *__restrict__ out, int64_t ldo) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / C::WN, wn = wave % C::WN;
     const int full = (int)(K >> 7), steps = (int)((K + 127) >> 7);  // whole stages, all stages
@@ -257,12 +257,12 @@ __device__ __forceinline__ void tile_unit(uint8_t *lds, const int8_t *__restrict
         if constexpr (4 * C::CB >= V) {
 #pragma unroll
             for (int c0 = 0; c0 < 4 * C::CB; c0 += V) {
-                typedef T vt __attribute__((ext_vector_type(V)));
+                typedef T vt __attribute__((ext_vector_type(V), aligned(sizeof(T))));
                 vt v;
 #pragma unroll
                 for (int c = 0; c < V; ++c)
                     v[c] = finish<T>(acc[i][(c0 + c) >> 2][(c0 + c) & 3], as, ws[c0 + c], bv[c0 + c], bias != nullptr);
-                if (vec && nb + c0 + V <= N) *reinterpret_cast<vt *>(o + c0) = v;
+                if (nb + c0 + V <= N) *reinterpret_cast<vt *>(o + c0) = v;  // any alignment
                 else {
 #pragma unroll
                     for (int c = 0; c < V; ++c)
@@ -300,7 +300,7 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 256 ? 2 : 1) void gemm_
                                                                      int64_t K, const int8_t *__restrict__ qw,
                                                                      const float *__restrict__ w_scale, int64_t N,
                                                                      const float *__restrict__ bias,
-                                                                     T *__restrict__ out, int64_t ldo, bool vec) {
+                                                                     T *__restrict__ out, int64_t ldo) {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kLds];
     const int64_t mt = (M + C::BM - 1) / C::BM, nt = (N + C::BN - 1) / C::BN;
     int64_t tm, tn;
@@ -308,7 +308,7 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 256 ? 2 : 1) void gemm_
     const int64_t m0 = tm * C::BM;
     const int rows = (int)((M - m0) < C::BM ? (M - m0) : C::BM);
     tile_unit<C, false, T>(lds, qa + m0 * K, a_scale + m0, [](int r) { return (int64_t)r; }, m0, rows, K, qw, w_scale, N,
-                           tn * C::BN, bias, out, ldo, vec);
+                           tn * C::BN, bias, out, ldo);
 }
 
 // ------------------------------------------------------------------ few rows
@@ -343,7 +343,7 @@ template <int NW, bool ONE, typename T, typename Walk>
 __device__ __forceinline__ void slice_walk(v4i (*red)[kMaxSliceWaves][64], Walk to_load, int64_t tiles,
                                            const int8_t *__restrict__ qa, const float *__restrict__ a_scale, int64_t K,
                                            int passes, int64_t N, const float *__restrict__ bias, T *__restrict__ out,
-                                           int64_t ldo, bool vec) {
+                                           int64_t ldo) {
     constexpr int D = 4 / NW > 0 ? 4 / NW : 1;  // tiles in the ring: about 4 windows, 8 KB a wave
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int W = blockDim.x >> 6;
@@ -441,14 +441,14 @@ red[turn][wave][lane] = acc;
                             if (m >= rows || src_row(m) < 0) return;
                             const int64_t nb = now.n0 + 4 * qd;
                             T *o = out + (slot0 + m) * ldo + nb;
-                            typedef T vt __attribute__((ext_vector_type(4)));
+                            typedef T vt __attribute__((ext_vector_type(4), aligned(sizeof(T))));
                             vt v;
 #pragma unroll
                             for (int r = 0; r < 4; ++r) {
                                 const int64_t n = nb + r < N ? nb + r : N - 1;
                                 v[r] = finish<T>(s[r], as, w_scale[n], bias ? bias[n] : 0.0f, bias != nullptr);
                             }
-                            if (vec && nb + 4 <= N) *reinterpret_cast<vt *>(o) = v;
+                            if (nb + 4 <= N) *reinterpret_cast<vt *>(o) = v;  // any alignment
                             else {
 #pragma unroll
                                 for (int r = 0; r < 4; ++r)
@@ -490,12 +490,12 @@ template <int NW, bool ONE, typename T>
 __global__ __launch_bounds__(64 * kMaxSliceWaves) void gemm_w8a8_slice_kernel(
     const int8_t *__restrict__ qa, const float *__restrict__ a_scale, int64_t M, int64_t K, int passes,
     const int8_t *__restrict__ qw, const float *__restrict__ w_scale, int64_t N, const float *__restrict__ bias,
-    T *__restrict__ out, int64_t ldo, bool vec) {
+    T *__restrict__ out, int64_t ldo) {
     __shared__ v4i red[2][kMaxSliceWaves][64];
     const int64_t nt = (N + 15) / 16, u0 = run_begin(blockIdx.x, gridDim.x, nt);
     const DenseWalk walk{qw + u0 * 16 * K, (N - u0 * 16) * K, u0 * 16, 16 * K, 0, (int)M, w_scale};
     slice_walk<NW, ONE, T>(red, walk, run_begin(blockIdx.x + 1, gridDim.x, nt) - u0, qa, a_scale, K, passes, N,
-                               bias, out, ldo, vec);
+                               bias, out, ldo);
 }
 
 // ------------------------------------------------------------------ per expert
@@ -604,7 +604,7 @@ __global__ __launch_bounds__(64 * kMaxSliceWaves) void grouped_w8a8_slice_kernel
     ExpertWalk walk{nullptr, 0, 0, 0, 0, K, N, R, max_slots, E, qw, w_scale, pfx, offsets, row_index};
     const int64_t b = uniform(u0 / nt);
     walk.at(b, uniform((u0 - b * nt) * 16));
-    slice_walk<NW, ONE, float>(red, walk, u1 - u0, qa, a_scale, K, passes, N, nullptr, out, N, N % 4 == 0);
+    slice_walk<NW, ONE, float>(red, walk, u1 - u0, qa, a_scale, K, passes, N, nullptr, out, N);
 }
 
 // Experts with more than lo slots on C's tiles: a persistent grid over (row block, column tile)
@@ -630,7 +630,7 @@ __global__ __launch_bounds__(C::kThreads) void grouped_w8a8_tile_kernel(
         const int64_t s0 = clamp_slots(offsets[e], max_slots) + C::BM * b;
         const int64_t left = clamp_slots(offsets[e + 1], max_slots) - s0;
         tile_unit<C, true, float>(lds, qa, a_scale, SlotRows{row_index, s0, R}, s0, left < C::BM ? (int)left : C::BM, K,
-                            qw + e * N * K, w_scale + e * N, N, tn * C::BN, nullptr, out, N, N % 4 == 0);
+                            qw + e * N * K, w_scale + e * N, N, tn * C::BN, nullptr, out, N);
         __syncthreads();  // the LDS stages are taken again by the next unit
     }
 }
@@ -648,11 +648,10 @@ namespace w4a8 {
 
 template <typename C, typename T>
 static hipError_t launch_tile(const int8_t *qa, const float *a_scale, int64_t M, int64_t K, const int8_t *qw,
-                              const float *w_scale, int64_t N, const float *bias, T *out, int64_t ldo, bool vec,
-                              hipStream_t stream) {
+                              const float *w_scale, int64_t N, const float *bias, T *out, int64_t ldo, hipStream_t stream) {
     const int64_t tiles = ((M + C::BM - 1) / C::BM) * ((N + C::BN - 1) / C::BN);
     hipLaunchKernelGGL((gemm_w8a8_tile_kernel<C, T>), dim3((uint32_t)tiles), dim3(C::kThreads), 0, stream, qa, a_scale,
-                       M, K, qw, w_scale, N, bias, out, ldo, vec);
+                       M, K, qw, w_scale, N, bias, out, ldo);
     return hipGetLastError();
 }
 
@@ -680,13 +679,12 @@ static Slices slices_of(int64_t K, int max_waves, int max_nw) {
 
 template <typename T>
 static hipError_t launch_slice(const int8_t *qa, const float *a_scale, int64_t M, int64_t K, const int8_t *qw,
-                               const float *w_scale, int64_t N, const float *bias, T *out, int64_t ldo, bool vec,
-                               hipStream_t stream) {
+                               const float *w_scale, int64_t N, const float *bias, T *out, int64_t ldo, hipStream_t stream) {
     const Slices s = slices_of(K, kMaxSliceWaves, 4);
     const int64_t grid = std::min<int64_t>((N + 15) / 16, kCus * (kMaxSliceWaves / s.waves));
 #define W4A8_SLICE(NN, ONE)                                                                                         \
     hipLaunchKernelGGL((gemm_w8a8_slice_kernel<NN, ONE, T>), dim3((uint32_t)grid), dim3(64 * s.waves), 0, stream, \
-                       qa, a_scale, M, K, s.passes, qw, w_scale, N, bias, out, ldo, vec)
+                       qa, a_scale, M, K, s.passes, qw, w_scale, N, bias, out, ldo)
     if (s.passes > 1) W4A8_SLICE(4, false);
     else if (s.nw == 1) W4A8_SLICE(1, true);
     else if (s.nw == 2) W4A8_SLICE(2, true);
@@ -700,24 +698,29 @@ template <typename T>
 static hipError_t gemm_w8a8_typed(const int8_t *qa, const float *a_scale, int64_t M, int64_t K, const int8_t *qw,
                                   const float *w_scale, int64_t N, const float *bias, T *out, int64_t ldo,
                                   hipStream_t stream) {
-    const bool vec = (uintptr_t)out % 16 == 0 && ldo * (int64_t)sizeof(T) % 16 == 0;
     // Few rows and a long k, or runs of at least four 16-channel tiles for every workgroup: k shared
     // out within the workgroup (K 16384, N 4096, one row: 18.7 us against 24.3 on 32 x 64 tiles;
     // K 4096, N 14336: 17.7 against 14.3).
     if (M <= 16 && (K > 8192 || N >= 16 * 4 * kCus))
-        return launch_slice(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream);
-    // Else the largest tile that nearly fills the CUs (and is no taller than M needs): a tile of 16
-    // times the area reads a quarter of the bytes per product, but 64 idle CUs of 256 cost more.
-    // M 512, K = N 8192: 128 x 128 (256 tiles) 41 us, 128 x 256 58, 64 x 64 68; M 77, K 4112, N 5003:
-    // 32 x 64 (237) 10 us, 64 x 64 (158) 14, 128 x 128 22.
-    auto fits = [&](int64_t bm, int64_t bn) {
-        return bm < 2 * M && ((M + bm - 1) / bm) * ((N + bn - 1) / bn) >= kCus * 7 / 8;
+        return launch_slice(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, stream);
+    // Else the tile form of the least expected time.  Per 256 tiles (one for every CU) and K 8192 the
+    // forms take about 100 us (256 x 256), 60 (128 x 256), 39 (128 x 128), 15.5 (64 x 64, and 5 once) and
+    // 10.7 (32 x 64, and 8 once), part rounds as whole ones: large tiles read less per product, small
+    // ones leave fewer CUs idle.  Measured against the other forms: M 512, K = N 8192 128 x 128 41 us
+    // (128 x 256 58, 64 x 64 68); M 77, K 4112, N 5003 32 x 64 10 us (64 x 64 14, 128 x 128 22); M 256, K 8192,
+    // N 28672 128 x 256 74 us (128 x 128 87, 256 x 256 106).
+    auto cost = [&](int64_t bm, int64_t bn, double round, double once) {
+        const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
+        return (double)((tiles + kCus - 1) / kCus) * round + once;
     };
-#define W4A8_TILE(C) launch_tile<C>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, vec, stream)
-    if (fits(256, 256)) return W4A8_TILE(Tile256);
-    if (fits(128, 256)) return W4A8_TILE(Tile128);
-    if (fits(128, 128)) return W4A8_TILE(Tile128n);
-    if (fits(64, 64)) return W4A8_TILE(Tile64);
+    const double c256 = cost(256, 256, 100.0, 0.0), c128 = cost(128, 256, 60.0, 0.0), c128n = cost(128, 128, 39.0, 0.0);
+    const double c64 = cost(64, 64, 15.5, 5.0), c32 = cost(32, 64, 10.7, 8.0);
+    const double least = std::min({c256, c128, c128n, c64, c32});
+#define W4A8_TILE(C) launch_tile<C>(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, stream)
+    if (c256 == least) return W4A8_TILE(Tile256);
+    if (c128 == least) return W4A8_TILE(Tile128);
+    if (c128n == least) return W4A8_TILE(Tile128n);
+    if (c64 == least) return W4A8_TILE(Tile64);
     return W4A8_TILE(Tile32);
 #undef W4A8_TILE
 }
