@@ -31,9 +31,9 @@ __device__ __forceinline__ int64_t clamp_slots(int64_t v, int64_t max_slots) {
 // ------------------------------------------------------------------ tile
 // A workgroup of WM x WN waves computes a BM x BN tile, each wave RB x CB blocks of 16 x 16 on
 // v_mfma_i32_16x16x64_i8 with the weights as the first operand: a lane then holds, of one row
-// m, four neighbouring output channels per block, and the weight rows of a wave's blocks are
-// taken so that its CB blocks make 4 CB neighbours (see wrow below), which it stores as whole
-// 16-byte pieces.
+// m, four neighbouring output channels per block.  The weight rows are dealt to the blocks so that
+// G blocks (16 bytes of outputs; see wrow) make 4 G neighbours of a lane and 16 G of a row's four
+// lanes: a store instruction writes 64-byte pieces.
 // Both operands go straight from memory into LDS (16 bytes per lane), 128 bytes of k per stage,
 // NST stages.  LDS rows are 128 bytes; the 16-byte chunk c of row r sits at chunk c ^ key(r), so
 // that the 16 rows of a fragment read fall in distinct banks.
@@ -67,10 +67,16 @@ struct Tile {
     static constexpr int kStageA = BM * 128, kStage = (BM + BN) * 128, kLds = NST * kStage;
     static_assert(LA * 8 * kWaves == BM && LB * 8 * kWaves == BN, "whole loads per wave");
     static_assert(kLds <= 160 * 1024, "LDS of one CU");
+    static __device__ int key_a(int r) { return (r >> 1) & 7; }
+};
+
+// G column blocks whose outputs of one lane are neighbours; their weight rows and LDS keys.
+template <int G>
+struct Deal {
     // the fragment row i (0..15) of a wave's column block cb is its weight row wrow(i, cb)
-    __device__ static int wrow(int i, int cb) { return 4 * CB * (i >> 2) + 4 * cb + (i & 3); }
-    __device__ static int key_a(int r) { return (r >> 1) & 7; }
-    __device__ static int key_b(int r) { return ((r >> 1) & 1) | (((r / (4 * CB)) & 3) << 1); }
+    static __device__ int wrow(int i, int cb) { return 16 * G * (cb / G) + 4 * G * (i >> 2) + 4 * (cb % G) + (i & 3); }
+    // chunk key of LDS row r: distinct over a fragment's 8 rows of one parity, the same for all blocks
+    static __device__ int key(int r) { return ((r >> 1) & 1) | (((r / (4 * G)) & 3) << 1); }
 };
 
 // src_row(r), r < rows: activation row of the tile's row r, or -1 (computed as row 0, not stored).
@@ -88,6 +94,8 @@ __device__ __forceinline__ void tile_unit(uint8_t *lds, const int8_t *__restrict
     const int full = (int)(K >> 7), steps = (int)((K + 127) >> 7);  // whole stages, all stages
     const int tail = (int)(K & 127) >> 4;                          // chunks of a last part stage
 
+    constexpr int V4 = 4 / (int)sizeof(T), G = C::CB >= V4 ? V4 : C::CB;  // blocks of a 16-byte store
+    using D = Deal<G>;
     constexpr int kReads = C::RB + C::CB, kMul = C::RB * C::CB, kLoads = C::LA + C::LB;
 
     // ---- loads: lane L of load j fills chunk L & 7 of row 8 (L? wave + j) + (L >> 3)
@@ -109,7 +117,7 @@ __device__ __forceinline__ void tile_unit(uint8_t *lds, const int8_t *__restrict
     for (int j = 0; j < C::LB; ++j) {
         const int r = 8 * (C::LB * wave + j) + (lane >> 3);
         const int64_t c = n0 + r < N ? r : N - 1 - n0;
-        bch[j] = (lane & 7) ^ C::key_b(r);
+        bch[j] = (lane & 7) ^ D::key(r);
         boff[j] = (uint32_t)(c * K) + 16u * (uint32_t)bch[j];
     }
     auto load_one = [&](int g, int st, int j) {  // load j of a whole stage
@@ -153,16 +161,16 @@ __device__ __forceinline__ void tile_unit(uint8_t *lds, const int8_t *__restrict
     int aofs[2], bofs[2];
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-        const int ra = wm * C::RB * 16 + fr, rw = wn * C::CB * 16 + C::wrow(fr, 0);
+        const int ra = wm * C::RB * 16 + fr, rw = wn * C::CB * 16 + D::wrow(fr, 0);
         aofs[ks] = ra * 128 + (((4 * ks + qd) ^ C::key_a(ra)) << 4);
-        bofs[ks] = C::kStageA + rw * 128 + (((4 * ks + qd) ^ C::key_b(rw)) << 4);
+        bofs[ks] = C::kStageA + rw * 128 + (((4 * ks + qd) ^ D::key(rw)) << 4);
     }
     struct Frags {
         v4i a[C::RB], b[C::CB];
     };
     auto read_one = [&](Frags &f, int st, int ks, int r) {
         const uint8_t *base = lds + st * C::kStage;
-        if (r < C::CB) f.b[r % C::CB] = *reinterpret_cast<const v4i *>(base + bofs[ks] + 512 * r);  // wrow steps by 4
+        if (r < C::CB) f.b[r % C::CB] = *reinterpret_cast<const v4i *>(base + bofs[ks] + 128 * D::wrow(0, r));
         else f.a[(r - C::CB) % C::RB] = *reinterpret_cast<const v4i *>(base + aofs[ks] + 2048 * (r - C::CB));
     };
     v4i acc[C::RB][C::CB] = {};
@@ -237,43 +245,39 @@ __device__ __forceinline__ void tile_unit(uint8_t *lds, const int8_t *__restrict
     half(f0, Yes{}, f1, st, 1, No{}, 0, 0);
     half(f1, No{}, f0, st, 0, No{}, 0, 0);
 
-    // ---- epilogue: lane l holds row 16 i + (l & 15) and, of block j, channels 4 CB (l >> 4) + 4 j + r
-    const int64_t nb = n0 + wn * C::CB * 16 + 4 * C::CB * qd;
-    float ws[4 * C::CB], bv[4 * C::CB];
+    // ---- epilogue: lane l holds row 16 i + (l & 15) and, of block j, weight rows wrow(4 (l >> 4) + r, j)
+    constexpr int V = 4 * G, kPieces = C::CB / G;
+    typedef T vt __attribute__((ext_vector_type(V), aligned(sizeof(T))));
+    const int64_t nb = n0 + wn * C::CB * 16 + V * qd;
+    float ws[kPieces][V], bv[kPieces][V];
 #pragma unroll
-    for (int c = 0; c < 4 * C::CB; ++c) {
-        const int64_t n = nb + c < N ? nb + c : N - 1;
-        ws[c] = w_scale[n];
-        bv[c] = bias ? bias[n] : 0.0f;
-    }
+    for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+            const int64_t n = nb + 4 * V * p + c < N ? nb + 4 * V * p + c : N - 1;
+            ws[p][c] = w_scale[n];
+            bv[p][c] = bias ? bias[n] : 0.0f;
+        }
 #pragma unroll
     for (int i = 0; i < C::RB; ++i) {
         const int m = wm * C::RB * 16 + 16 * i + fr;
         const int64_t row = m < rows ? src_row(m) : -1;
         if (row < 0) continue;
         const float as = a_scale[row];
-        T *o = out + (slot0 + m) * ldo + nb;
-        constexpr int V = 16 / sizeof(T);  // elements of a 16-byte store
-        if constexpr (4 * C::CB >= V) {
 #pragma unroll
-            for (int c0 = 0; c0 < 4 * C::CB; c0 += V) {
-                typedef T vt __attribute__((ext_vector_type(V), aligned(sizeof(T))));
-                vt v;
+        for (int p = 0; p < kPieces; ++p) {
+            const int64_t n = nb + 4 * V * p;
+            T *o = out + (slot0 + m) * ldo + n;
+            vt v;
+#pragma unroll
+            for (int c = 0; c < V; ++c)
+                v[c] = finish<T>(acc[i][G * p + (c >> 2)][c & 3], as, ws[p][c], bv[p][c], bias != nullptr);
+            if (n + V <= N) *reinterpret_cast<vt *>(o) = v;  // any alignment
+            else {
 #pragma unroll
                 for (int c = 0; c < V; ++c)
-                    v[c] = finish<T>(acc[i][(c0 + c) >> 2][(c0 + c) & 3], as, ws[c0 + c], bv[c0 + c], bias != nullptr);
-                if (nb + c0 + V <= N) *reinterpret_cast<vt *>(o + c0) = v;  // any alignment
-                else {
-#pragma unroll
-                    for (int c = 0; c < V; ++c)
-                        if (nb + c0 + c < N) o[c0 + c] = v[c];
-                }
+                    if (n + c < N) o[c] = v[c];
             }
-        } else {
-#pragma unroll
-            for (int c = 0; c < 4 * C::CB; ++c)
-                if (nb + c < N)
-                    o[c] = finish<T>(acc[i][c >> 2][c & 3], as, ws[c], bv[c], bias != nullptr);
         }
     }
 }
