@@ -14,6 +14,10 @@
 // An expert whose logit or bias is -inf has v = key = -inf and weight 0.  Scores and keys are
 // held in fp64: two experts' keys often differ by less than an fp32 ulp, and the picks
 // should be those of the formula.
+//
+// A few MB at most are read and written; the time is latency and instructions.  E 384, k 8,
+// sigmoid + bias: one token 6.5 us (one launch), 4096 tokens 11 us here and 13 us in the placing;
+// 20011 tokens, E 160, softmax in 8 groups: 27 + 20 us (every VALU cycle used).
 #include <type_traits>
 
 #include "w8_internal.hpp"
@@ -283,7 +287,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_scored_kernel(const L *__
 // pairs of all lower experts.  Each wave owns a contiguous run of pairs and reads it twice (to count,
 // then to place), 256 pairs at a time, four neighbours per lane, counting with ballots.  The ids
 // come from L2, E times over, which for some 10^5 pairs costs less than a scan over chunks with
-// its extra launches.
+// its extra launches.  32768 pairs, E 384: 12.7 us (71 with a contiguous run of pairs per thread).
 // shared_T >= 0: a shared expert with that many slots follows.
 typedef int32_t ids4 __attribute__((ext_vector_type(4), aligned(4)));
 template <int THREADS>

@@ -5,7 +5,14 @@
 //     out[m][n]  = T(fp32(isum) * a_scale[m] * w_scale[n] + bias[n])
 //
 // The same product runs dense, and per expert over the slot lists of the router.  The sums are
-// integers, so neither the order of k nor a split of it changes a result.
+// integers, so neither the order of k nor a split of it changes a result: every loop gives the
+// same bytes.
+//
+// Two loops.  Up to 16 rows (slice_walk) the weights are read once and are the whole cost: 235 MB
+// in 39.7 us (K 8192, N 28672, one row), 5.9 TB/s, where a large copy moves 5.1 TB/s.  More rows go
+// through LDS tiles (tile_unit): 4096 x 8192 x 8192 in 199-218 us on different boxes, 2.5-2.8 POPS;
+// the matrix pipes alone, fed from registers with such codes, ran at 3.9 POPS (the clock drops to
+// 1.9 GHz under them).
 #include <algorithm>
 #include <type_traits>
 
@@ -41,6 +48,11 @@ __device__ __forceinline__ int64_t clamp_slots(int64_t v, int64_t max_slots) {
 // before it is multiplied, so the one barrier per stage stands between the halves of stage g:
 // there every wave holds the fragments of its second half in registers (the stage's buffer is
 // free for stage g + NST) and stage g + 1 has landed (its first half may be read).
+// Measured on 256 x 256, M 4096, K = N 8192 (MFMA busy 76% of the CUs' busy cycles, no LDS bank
+// conflicts, 20% of the L2 reads miss): without the loads 164 us, without the LDS reads 231, with
+// every line in L2 189.  Not kept: stages of 64 bytes, five of them (237 us: twice the barriers, half
+// lines from L2); four waves of 128 x 128 (229); two 128 x 256 workgroups of four waves per CU
+// (279); 32x32x32 products (266); raised wave priority around the products (231).
 typedef __attribute__((address_space(3))) void *lds_ptr_t;
 typedef const __attribute__((address_space(1))) void *glb_ptr_t;
 
@@ -177,7 +189,8 @@ __device__ __forceinline__ void tile_unit(uint8_t *lds, const int8_t *__restrict
     // Products of the half in `now`; after each of them one fragment of the half after it (stage st,
     // half ks, if rd) and after every second one a load of stage g into the buffer sti (if ld), in
     // just this order: the reads are then back long before the half ends, and no burst of loads
-    // holds up the products.  (The compiler's own order put the reads behind the loads, at the end.)
+    // holds up the products.  (The compiler's own order put the reads behind the loads, at the end:
+    // 218 us against 210 at M 4096, K = N 8192.)
     auto half = [&](const Frags &now, auto rd, Frags &then, int st, int ks, auto ld, int g, int sti) {
         // read r and load d follow these products (a small tile has fewer products than reads or loads)
         constexpr auto read_at = [](int r) { return kMul > kReads + 2 ? r + 2 : r * kMul / kReads; };
@@ -329,6 +342,8 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 256 ? 2 : 1) void gemm_
 // lanes, written to half of them.
 // Channels past N and bytes past the array read as 0 (the descriptor ends with the array); k past
 // K and the windows that a wave has no share of are zeros on the activations' side.
+// K 8192, N 28672: one row 39.7 us, 16 rows 42.6 (49.5 and 76 with the rows read from the caches per
+// window and one tile per workgroup; 56 and 60 with a ring of 8 windows, which spills).
 template <int BANKS>
 __device__ __forceinline__ v4i ror8_into(v4i old, v4i src) {
     v4i r;
@@ -594,6 +609,8 @@ struct ExpertWalk {
 };
 
 // Experts of up to 16 slots: a workgroup's run of tiles goes through one expert after the other.
+// Bound by the weights: 64 tokens, top 8 of 384, K 7168, N 4096 (6.4 GB) 0.95 ms here, 1.05 ms on
+// persistent 32 x 64 tiles; one token 44 us.
 template <int NW, bool ONE>
 __global__ __launch_bounds__(64 * kMaxSliceWaves) void grouped_w8a8_slice_kernel(
     const int8_t *__restrict__ qa, const float *__restrict__ a_scale, int64_t R, const int32_t *__restrict__ row_index,
@@ -613,7 +630,10 @@ __global__ __launch_bounds__(64 * kMaxSliceWaves) void grouped_w8a8_slice_kernel
 
 // Experts with more than lo slots on C's tiles: a persistent grid over (row block, column tile)
 // units, an expert's row blocks next to each other on one XCD, so that its weights come
-// through one L2.
+// through one L2.  4096 tokens, top 8 of 384, K 7168, N 4096 (338 experts here, 10 GB) 2.13 ms: 4.9
+// TB/s of weights with 62% of the products' time behind them.  A 64 x 256 form for 17-64 slots and this
+// one for the rest took as long (0.91 + 1.23 ms) with a launch more, 256 x 256 above 128 slots 5%
+// longer, two stages instead of three 12%, loads that warm L2 ahead 17%.
 template <typename C>
 __global__ __launch_bounds__(C::kThreads) void grouped_w8a8_tile_kernel(
     const int8_t *__restrict__ qa, const float *__restrict__ a_scale, int64_t R, const int32_t *__restrict__ row_index,
