@@ -83,6 +83,16 @@ def test_expert_counts(E, k, n, keep, lead, bias):
         n_groups=n, topk_groups=keep, group_lead=lead, with_shared=not bias)
 
 
+@pytest.mark.parametrize("T", [1, 3, 16])
+@pytest.mark.parametrize("E,k,n,keep,lead", [(1, 1, 1, 1, 1), (60, 8, 5, 2, 2), (384, 8, 1, 1, 1), (513, 32, 27, 20, 2),
+                                             (1000, 32, 50, 10, 2), (1024, 32, 64, 33, 1)])
+def test_few_tokens(T, E, k, n, keep, lead):
+    """The one-launch form over the expert counts, its pairs up to 16 tokens of 32."""
+    run(logits_of(E + T, T, E), k, score="softmax", bias=bias_of(E, E), n_groups=n, topk_groups=keep, group_lead=lead,
+        with_shared=True)
+    run(logits_of(E + T, T, E), k, score="sigmoid", n_groups=n, topk_groups=keep, group_lead=lead, renorm=False)
+
+
 @pytest.mark.parametrize("dtype", sorted(TYPES))
 @pytest.mark.parametrize("pad", [0, 1, 24])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])

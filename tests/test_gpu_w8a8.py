@@ -247,6 +247,25 @@ def test_grouped_no_slots_and_clamped_offsets():
         o.close(got[s], ref, bound, 0.0, 0.0)
 
 
+def test_grouped_offsets_that_are_not_ascending():
+    """Offsets that go back and forth: the call ends, writes rows below max_slots only, and each written row is the
+    product with one of the experts that claim it."""
+    w4 = w4mod()
+    rng = np.random.default_rng(11)
+    S, K, N, E = 300, 64, 48, 16
+    qa, sa, qw, sw = codes(rng, S, K), scales(rng, S), codes(rng, E, N, K), np.stack([scales(rng, N) for _ in range(E)])
+    off = np.array([0, 2 ** 31 - 1] * 8 + [-5], np.int32)
+    buf = torch.full((S + 20, N), -7.0, device=cuda())
+    w4.moe_grouped_gemm_w8a8(to_dev(qa), to_dev(sa), None, to_dev(off), to_dev(qw), to_dev(sw), S, out=buf[:S])
+    got = to_host(buf)
+    assert (got[S:] == -7.0).all()
+    near = np.zeros((S, N), bool)
+    for e in range(E):
+        ref, bound = o.product(qa, sa, qw[e], sw[e])
+        near |= np.abs(got[:S] - ref) <= bound
+    assert (near | (got[:S] == -7.0)).all()
+
+
 def test_grouped_large_arrays():
     """Expert weights past 2^32 bytes and activation rows past 2^32 bytes: rows and experts on both sides."""
     w4 = w4mod()

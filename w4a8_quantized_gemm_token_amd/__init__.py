@@ -423,7 +423,8 @@ def gemm_w8a8(qa, a_scale, qw, w_scale, bias=None, out_dtype=None, out=None):
 
 
 def prepare_gemm_w8a8(qa, a_scale, qw, w_scale, out, bias=None) -> Launch:
-    """Prepared w4a8_gemm_w8a8 writing into a preallocated out [M][N] (float32, float16 or bfloat16)."""
+    """Prepared w4a8_gemm_w8a8 writing into a preallocated out [M][N] (float32, float16 or bfloat16).  Called
+    with the tensors' device current, as the other prepared calls."""
     return Launch("w4a8_gemm_w8a8", _gemm_w8a8_args(qa, a_scale, qw, w_scale, bias, out),
                   (qa, a_scale, qw, w_scale, bias, out))
 

@@ -532,38 +532,40 @@ struct SlotRows {
 
 // Work units of the experts with lo < slots <= hi: ceil(slots / bm) row blocks each, times nt column
 // tiles.  pfx[0 .. E] receives the exclusive prefix of the row blocks over experts (whole
-// workgroup; E <= 1024); pfx[kMaxE + 1 ..] is scratch.
-constexpr int kPfx = kMaxE + 1 + 16;
+// workgroup; E <= 1024), cut off at the most there can be of ascending offsets, so that offsets that
+// are not ascending cost no more work than others; pfx[kMaxE + 1 ..] is scratch.
+constexpr int kPfx = kMaxE + 1 + 2 * 16 + 1;
 __device__ __forceinline__ void block_prefix(int32_t *pfx, const int32_t *__restrict__ offsets, int32_t E,
                                              int64_t max_slots, int lo, int hi, int bm) {
-    int32_t *part = pfx + kMaxE + 1;
+    int64_t *part = reinterpret_cast<int64_t *>(pfx + kMaxE + 2);  // 8-byte aligned, as pfx is
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nw = blockDim.x >> 6;
     const int per = (E + blockDim.x - 1) / blockDim.x;  // <= 16 experts per thread
-    auto blocks = [&](int e) -> int32_t {
+    const int64_t most = E + max_slots / bm;            // < 2^31
+    auto blocks = [&](int e) -> int64_t {
         const int64_t c = clamp_slots(offsets[e + 1], max_slots) - clamp_slots(offsets[e], max_slots);
-        return c > lo && c <= hi ? (int32_t)((c + bm - 1) / bm) : 0;
+        return c > lo && c <= hi ? (c + bm - 1) / bm : 0;
     };
     const int e0 = tid * per, e1 = e0 + per < E ? e0 + per : E;
-    int32_t own = 0;
+    int64_t own = 0;
     for (int e = e0; e < e1; ++e) own += blocks(e);
-    int32_t incl = own;
+    int64_t incl = own;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-        const int32_t o = __shfl_up(incl, off, 64);
+        const int64_t o = __shfl_up(incl, off, 64);
         if (lane >= off) incl += o;
     }
     if (lane == 63) part[wave] = incl;
     __syncthreads();
-    int32_t run = incl - own;
+    int64_t run = incl - own;
     for (int w = 0; w < wave; ++w) run += part[w];
     for (int e = e0; e < e1; ++e) {
-        pfx[e] = run;
+        pfx[e] = (int32_t)(run < most ? run : most);
         run += blocks(e);
     }
     if (tid == 0) {
-        int32_t total = 0;
+        int64_t total = 0;
         for (int w = 0; w < nw; ++w) total += part[w];
-        pfx[E] = total;
+        pfx[E] = (int32_t)(total < most ? total : most);
     }
     __syncthreads();
 }
@@ -617,7 +619,7 @@ __global__ __launch_bounds__(64 * kMaxSliceWaves) void grouped_w8a8_slice_kernel
     const int32_t *__restrict__ offsets, int32_t E, int64_t K, int passes, const int8_t *__restrict__ qw,
     const float *__restrict__ w_scale, int64_t N, int64_t max_slots, int hi, float *__restrict__ out) {
     __shared__ v4i red[2][kMaxSliceWaves][64];
-    __shared__ int32_t pfx[kPfx];
+    __shared__ __attribute__((aligned(8))) int32_t pfx[kPfx];
     block_prefix(pfx, offsets, E, max_slots, 0, hi, 16);
     const int64_t nt = (N + 15) / 16, units = uniform(pfx[E]) * nt;
     const int64_t u0 = run_begin(blockIdx.x, gridDim.x, units), u1 = run_begin(blockIdx.x + 1, gridDim.x, units);
