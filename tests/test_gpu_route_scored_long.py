@@ -1,0 +1,85 @@
+"""GPU tests of the scored router over very long batches and hot experts: the tables against sorting on the device,
+the weights against fp64, and the time per pair."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from tests import w8_oracle as o
+from tests.gpu_common import cuda, to_host
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    yield
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+
+
+def w4mod():
+    import w4a8_quantized_gemm_token_amd as w4
+    return w4
+
+
+def check_tables(ids, E, off, perm, rows, sop):
+    """The tables of ids [T][k] on the device: stable order of the pairs by expert."""
+    T, k = ids.shape
+    flat = ids.reshape(-1)
+    order = torch.sort(flat, stable=True).indices
+    assert torch.equal(perm.long(), order)
+    counts = torch.stack([(flat == e).sum() for e in range(E)])
+    assert off[:E + 1].tolist() == [0] + counts.cumsum(0).tolist()
+    assert torch.equal(rows[:T * k].long(), order // k)
+    back = torch.empty_like(order)
+    back[order] = torch.arange(T * k, device=ids.device)
+    assert torch.equal(sop.long(), back)
+
+
+def hot_logits(T, E, hot, share, gen):
+    """Tokens of which `share` want the experts 0 .. hot - 1 first, the others any."""
+    x = torch.randn(T, E, device=cuda(), generator=gen)
+    x[:, :hot] += 50.0 * (torch.rand(T, 1, device=cuda(), generator=gen) < share)
+    return x
+
+
+@pytest.mark.parametrize("T,E,k,share", [(700, 40, 3, 1.0), (3001, 40, 3, 0.7), (70001, 40, 3, 1.0), (100003, 40, 3, 0.5),
+                                         (262144, 8, 2, 0.999), (250000, 160, 6, 0.05)])
+def test_hot_buckets(T, E, k, share):
+    """Buckets that take many rounds of a workgroup's list, dense and sparse in the ids."""
+    gen = torch.Generator(device=cuda()).manual_seed(T)
+    x = hot_logits(T, E, k, share, gen)
+    ids, w, off, perm, rows, sop = w4mod().moe_route_scored(x, k, score="sigmoid", renorm=False, with_shared=True)
+    assert torch.equal(ids.long(), torch.sort(x, dim=1, descending=True, stable=True).indices[:, :k])
+    check_tables(ids, E, off, perm, rows, sop)
+    assert int(off[E + 1]) == T * k + T and torch.equal(rows[T * k:].long(), torch.arange(T, device=cuda()))
+
+
+def test_time_is_linear_in_the_pairs():
+    """Every token picks the same experts: 8 times the tokens take about 8 times as long (1.0 and 8.0 ms), where
+    reading all ids again for every 8192 pairs of a bucket took 60 times as long (2.6 and 156 ms)."""
+    w4 = w4mod()
+    E, k = 40, 3
+    took = []
+    for T in (1 << 18, 1 << 21):
+        x = torch.arange(E, dtype=torch.float32, device=cuda()).repeat(T, 1)
+        outs = w4.moe_route_scored(x, k)
+        call = w4.prepare_moe_route_scored(x, k, outs)
+        best = []
+        for _ in range(3):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            call()
+            b.record()
+            torch.cuda.synchronize()
+            best.append(a.elapsed_time(b))
+        took.append(min(best))
+        for j in range(k):
+            assert int(outs[2][E - k + j]) == j * T
+            assert torch.equal(outs[3][j * T:(j + 1) * T], torch.arange(T, device=cuda(), dtype=torch.int32) * k + k - 1 - j)
+    assert took[1] < 24 * took[0], took

@@ -301,14 +301,15 @@ __global__ __launch_bounds__(THREADS) void place_kernel(const int32_t *__restric
     const int32_t e = blockIdx.x;
     const int64_t chunks = ((int64_t)P + kChunk - 1) / kChunk;
     const int64_t p0 = chunks * wave / kWaves * kChunk, p1 = chunks * (wave + 1) / kWaves * kChunk;
-    // calls f(c, ids of the pairs c + 4 lane + 0..3) for the wave's chunks, with the loads of 8 or 2 of
-    // them in flight (their latency is most of the time); past the end the ids are above all
-    auto walk = [&](auto f) {
+    // calls f(c, ids of the pairs c + 4 lane + 0..3) for the wave's chunks from `from` on while more(), with
+    // the loads of 8 or 2 of them in flight (their latency is most of the time); past the end the ids
+    // are above all
+    auto walk = [&](int64_t from, auto more, auto f) {
         const int64_t whole = p1 < P ? p1 : P;
-        int64_t c = p0;
+        int64_t c = from;
         auto batch = [&](auto deep) {
             constexpr int D = decltype(deep)::value;
-            for (; c + D * kChunk <= whole; c += D * kChunk) {
+            for (; c + D * kChunk <= whole && more(); c += D * kChunk) {
                 ids4 v[D];
 #pragma unroll
                 for (int d = 0; d < D; ++d) v[d] = *reinterpret_cast<const ids4 *>(ids + c + d * kChunk + 4 * lane);
@@ -318,7 +319,7 @@ __global__ __launch_bounds__(THREADS) void place_kernel(const int32_t *__restric
         };
         batch(std::integral_constant<int, 8>{});
         batch(std::integral_constant<int, 2>{});
-        for (; c < p1; c += kChunk) {
+        for (; c < p1 && more(); c += kChunk) {
             ids4 v;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -330,7 +331,7 @@ __global__ __launch_bounds__(THREADS) void place_kernel(const int32_t *__restric
         }
     };
     int32_t below = 0, own = 0;
-    walk([&](int64_t, const ids4 &v) {
+    walk(p0, [] { return true; }, [&](int64_t, const ids4 &v) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             below += __popcll(__ballot(v[j] < e));
@@ -357,27 +358,39 @@ __global__ __launch_bounds__(THREADS) void place_kernel(const int32_t *__restric
     }
     // The expert's pairs go through a list in LDS, kList of them a round, so that the scattered
     // writes and the division are made by full waves, not by the one lane in 64 that found a pair.
+    // A wave starts a round in the chunk where its last one filled the list, so each id is read a
+    // bounded number of times whatever the length of the bucket (2^21 tokens of 3 pairs in the same
+    // three buckets: 8.0 ms, 156 with every round from the start).  A single round keeps no such
+    // place (24 us against 25 for 32768 pairs, E 384).
     const uint64_t lt = (1ull << lane) - 1;
-    for (int32_t base = 0; base < total; base += kList) {
-        int32_t next = before - base;  // list place of this wave's next pair
+    int64_t at = p0;
+    int32_t rank = before;  // number of the expert's pairs before the chunk `at`
+    auto round = [&](int32_t base, auto single) {
+        constexpr bool kSingle = decltype(single)::value;
+        int32_t next = rank - base;  // list place of this wave's next pair
         if (own > 0)
-            walk([&](int64_t c, const ids4 &v) {
+            walk(at, [&] { return kSingle || next < kList; }, [&](int64_t c, const ids4 &v) {
                 uint64_t m[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) m[j] = __ballot(v[j] == e);
-                if (!(m[0] | m[1] | m[2] | m[3])) return;
-                int32_t to = next;
+                if (m[0] | m[1] | m[2] | m[3]) {
+                    int32_t to = next;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    to += __popcll(m[j] & lt);
-                    next += __popcll(m[j]);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (v[j] == e) {
-                        if (to >= 0 && to < kList) list[to] = (int32_t)(c + 4 * lane + j);
-                        ++to;
+                    for (int j = 0; j < 4; ++j) {
+                        to += __popcll(m[j] & lt);
+                        next += __popcll(m[j]);
                     }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (v[j] == e) {
+                            if (to >= 0 && to < kList) list[to] = (int32_t)(c + 4 * lane + j);
+                            ++to;
+                        }
+                }
+                if (!kSingle && next <= kList) {  // else the next round takes this chunk again
+                    at = c + kChunk;
+                    rank = base + next;
+                }
             });
         __syncthreads();
         const int32_t n = total - base < kList ? total - base : kList;
@@ -388,7 +401,10 @@ __global__ __launch_bounds__(THREADS) void place_kernel(const int32_t *__restric
             if (slot_row) slot_row[slot] = p / k;
         }
         __syncthreads();
-    }
+    };
+    if (total <= kList) round(0, std::true_type{});
+    else
+        for (int32_t base = 0; base < total; base += kList) round(base, std::false_type{});
     if (slot_row)
         for (int64_t t = (int64_t)e * THREADS + tid; t < shared_T; t += (int64_t)E * THREADS)
             slot_row[P + t] = (int32_t)t;
