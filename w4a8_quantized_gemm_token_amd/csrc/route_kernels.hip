@@ -383,7 +383,9 @@ __global__ __launch_bounds__(THREADS) void place_kernel(const int32_t *__restric
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         if (v[j] == e) {
-                            if (to >= 0 && to < kList) list[to] = (int32_t)(c + 4 * lane + j);
+                            const int32_t p = (int32_t)(c + 4 * lane + j);
+                            if (kSingle) list[to & (kList - 1)] = p;  // to < total
+                            else if (to >= 0 && to < kList) list[to] = p;
                             ++to;
                         }
                 }
