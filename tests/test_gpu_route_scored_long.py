@@ -83,3 +83,20 @@ def test_time_is_linear_in_the_pairs():
             assert int(outs[2][E - k + j]) == j * T
             assert torch.equal(outs[3][j * T:(j + 1) * T], torch.arange(T, device=cuda(), dtype=torch.int32) * k + k - 1 - j)
     assert took[1] < 24 * took[0], took
+
+
+def test_more_tokens_than_a_launch_has_threads_for():
+    """2^26 tokens and some: a wave for each is 2^32 threads, more than one launch may have."""
+    T, E = (1 << 26) + 5, 8
+    gen = torch.Generator(device=cuda()).manual_seed(1)
+    x = torch.empty(T, E, dtype=torch.float16, device=cuda()).normal_(generator=gen)
+    ids, w, off, perm, rows, sop = w4mod().moe_route_scored(x, 1, score="sigmoid", renorm=False)
+    best = x.amax(1)
+    want = torch.full((T,), E, dtype=torch.int32, device=cuda())
+    for e in reversed(range(E)):
+        want[x[:, e] == best] = e
+    assert torch.equal(ids[:, 0], want)
+    ref = torch.sigmoid(best.double())
+    # fp64 scores, then one rounding to fp32
+    assert bool(((w[:, 0].double() - ref).abs() <= 1.0001 * o.U * ref).all())
+    check_tables(ids, E, off, perm, rows, sop)

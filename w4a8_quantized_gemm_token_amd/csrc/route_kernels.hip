@@ -468,7 +468,8 @@ template <typename L>
 static void route_typed(const L *logits, int64_t ldl, const float *bias, int64_t T, int32_t E, int64_t shared_T,
                         const RouteCfg &cfg, int32_t *ids, float *w, int32_t *offsets, int32_t *perm,
                         int32_t *slot_row, int32_t *slot_of_pair, bool one, hipStream_t stream) {
-    const dim3 grid((uint32_t)((T + kRouteWaves - 1) / kRouteWaves)), block(kRouteThreads);
+    // one launch per kLaunchTokens: its threads, 64 a token, have to stay below 2^32
+    constexpr int64_t kLaunchTokens = 1ll << 24;
     const int per = (E + kWave - 1) / kWave;
 #define W4A8_RS(PP)                                                                                                  \
     do {                                                                                                             \
@@ -477,8 +478,12 @@ static void route_typed(const L *logits, int64_t ldl, const float *bias, int64_t
                                bias, (int32_t)T, E, cfg, (int32_t)shared_T, ids, w, offsets, perm, slot_row,         \
                                slot_of_pair);                                                                        \
         else                                                                                                         \
-            hipLaunchKernelGGL((route_scored_kernel<PP, L>), grid, block, 0, stream, logits, ldl, bias, T, E, cfg,   \
-                               ids, w);                                                                              \
+            for (int64_t t = 0; t < T; t += kLaunchTokens) {                                                         \
+                const int64_t n = T - t < kLaunchTokens ? T - t : kLaunchTokens;                                     \
+                hipLaunchKernelGGL((route_scored_kernel<PP, L>), dim3((uint32_t)((n + kRouteWaves - 1) / kRouteWaves)), \
+                                   dim3(kRouteThreads), 0, stream, logits + t * ldl, ldl, bias, n, E, cfg,           \
+                                   ids + t * cfg.topk, w + t * cfg.topk);                                            \
+            }                                                                                                        \
     } while (0)
     if (per <= 1) W4A8_RS(1);
     else if (per <= 2) W4A8_RS(2);
