@@ -675,8 +675,17 @@ namespace w4a8 {
 template <typename C, typename T>
 static hipError_t launch_tile(const int8_t *qa, const float *a_scale, int64_t M, int64_t K, const int8_t *qw,
                               const float *w_scale, int64_t N, const float *bias, T *out, int64_t ldo, hipStream_t stream) {
-    const int64_t tiles = ((M + C::BM - 1) / C::BM) * ((N + C::BN - 1) / C::BN);
-    hipLaunchKernelGGL((gemm_w8a8_tile_kernel<C, T>), dim3((uint32_t)tiles), dim3(C::kThreads), 0, stream, qa, a_scale,
+    const int64_t mt = (M + C::BM - 1) / C::BM, nt = (N + C::BN - 1) / C::BN;
+    if (mt * nt * C::kThreads >= 1ll << 32) {
+        // a launch has to have fewer than 2^32 threads: two calls, with the longer side halved
+        const int64_t m = mt >= nt ? mt / 2 * C::BM : 0, n = mt >= nt ? 0 : nt / 2 * C::BN;
+        const hipError_t err = launch_tile<C>(qa, a_scale, mt >= nt ? m : M, K, qw, w_scale, mt >= nt ? N : n, bias, out,
+                                              ldo, stream);
+        if (err != hipSuccess) return err;
+        return launch_tile<C>(qa + m * K, a_scale + m, M - m, K, qw + n * K, w_scale + n, N - n,
+                              bias ? bias + n : nullptr, out + m * ldo + n, ldo, stream);
+    }
+    hipLaunchKernelGGL((gemm_w8a8_tile_kernel<C, T>), dim3((uint32_t)(mt * nt)), dim3(C::kThreads), 0, stream, qa, a_scale,
                        M, K, qw, w_scale, N, bias, out, ldo);
     return hipGetLastError();
 }
