@@ -107,3 +107,35 @@ def test_oracle_mistakes_are_caught():
     for bad in (o.product(wrong, sa, qw, sw, b)[0], o.product(qa, sa, qw, sw)[0], ref * (1 + 2.0 ** -9)):
         with pytest.raises(AssertionError):
             o.close(bad, ref, bound, 0.0, 0.0)
+
+
+# ------------------------------------------------------------------ devices
+def test_calls_run_on_their_tensors_device(monkeypatch):
+    """Each call makes its tensors' device the current one while it launches: the library launches on the
+    current device."""
+    torch = pytest.importorskip("torch")
+    entered, launched = [], []
+
+    class Guard:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            entered.append(self.device)
+
+        def __exit__(self, *_):
+            entered.pop()
+
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    monkeypatch.setattr(w4, "_call", lambda name, *args: launched.append((name, list(entered))))
+    monkeypatch.setattr(w4, "_dev_ptr", lambda t: None)
+    monkeypatch.setattr(w4, "_dev_rows_ptr", lambda t: None)
+    monkeypatch.setattr(w4, "_stream", lambda device=None: None)
+    z, i8, i32 = torch.zeros, torch.int8, torch.int32
+    w4.quantize_weights_w8(z(8, 16))
+    w4.gemm_w8a8(z(2, 16, dtype=i8), z(2), z(8, 16, dtype=i8), z(8))
+    w4.moe_route_scored(z(2, 8), 3)
+    w4.moe_grouped_gemm_w8a8(z(2, 16, dtype=i8), z(2), None, z(3, dtype=i32), z(2, 8, 16, dtype=i8), z(2, 8), 2)
+    assert [name for name, _ in launched] == ["w4a8_quantize_act", "w4a8_gemm_w8a8", "w4a8_moe_route_scored",
+                                              "w4a8_moe_grouped_gemm_w8a8"]
+    assert all(devices == [torch.device("cpu")] for _, devices in launched), launched

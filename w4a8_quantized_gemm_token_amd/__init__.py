@@ -390,7 +390,8 @@ def _is(t, shape, dtype, what):
 def quantize_weights_w8(W):
     """W float32 [N][K] (device) -> (qw int8 [N][K], w_scale float32 [N]): symmetric 8-bit codes per
     output channel, which is the row quantizer of the activations run over W's rows."""
-    return quantize_act(W)
+    with _torch().cuda.device(W.device):
+        return quantize_act(W)
 
 
 def _gemm_w8a8_args(qa, a_scale, qw, w_scale, bias, out):
