@@ -1,10 +1,11 @@
-"""GPU tests of the 8-bit product's forms that its sizes alone do not reach: launches cut in two."""
+"""GPU tests of the 8-bit product by form: every split of k of the few-row loop, launches cut in two."""
 from __future__ import annotations
 
 import numpy as np
 import pytest
 
-from tests.gpu_common import cuda, to_dev, to_host
+from tests.gpu_common import cuda
+from tests.test_gpu_w8a8 import dense, grouped
 
 pytestmark = pytest.mark.gpu
 
@@ -23,6 +24,22 @@ def _gpu():
 def w4mod():
     import w4a8_quantized_gemm_token_amd as w4
     return w4
+
+
+# k by which the few-row loop gives each wave 1, 2, 3 or 4 windows of 128 in one pass, or takes several passes;
+# with and without a part window, waves and windows without a share, and the full 16 waves
+FEW_ROW_K = [144, 2048, 2064, 3600, 4096, 2576, 4112, 4224, 5376, 6016, 6144, 3968, 7152, 7168, 8192, 8208, 24592]
+
+
+@pytest.mark.parametrize("K", FEW_ROW_K)
+@pytest.mark.parametrize("M", [1, 7, 16])
+def test_few_rows_every_split_of_k(M, K):
+    dense(np.random.default_rng(K + M), M, K, 16390, M == 7, "bf16" if M == 16 else "f32")
+
+
+@pytest.mark.parametrize("K", FEW_ROW_K)
+def test_few_slots_every_split_of_k(K):
+    grouped(np.random.default_rng(K), [1, 16, 0, 3, 9, 2, 16, 1], K, 1552)
 
 
 def repeated(block, n):

@@ -139,3 +139,24 @@ def test_calls_run_on_their_tensors_device(monkeypatch):
     assert [name for name, _ in launched] == ["w4a8_quantize_act", "w4a8_gemm_w8a8", "w4a8_moe_route_scored",
                                               "w4a8_moe_grouped_gemm_w8a8"]
     assert all(devices == [torch.device("cpu")] for _, devices in launched), launched
+
+
+# ------------------------------------------------------------------ which sizes the GPU tests run
+def split_of_k(K, max_waves=16, max_nw=4):
+    """(windows per wave, more than one pass) of the few-row loop: the launcher's rule, written again."""
+    windows = -(-K // 128)
+    passes = -(-windows // (max_waves * max_nw))
+    per = -(-windows // passes)
+    if passes > 1:
+        return max_nw, True
+    fits = [nw for nw in range(1, max_nw + 1) if -(-per // nw) <= max_waves]
+    return min(fits, key=lambda nw: (-(-per // nw) * nw - per, nw)), False
+
+
+def test_gpu_tests_reach_every_split_of_k():
+    pytest.importorskip("torch")
+    from tests.test_gpu_w8a8_forms import FEW_ROW_K
+    every = {(1, False), (2, False), (3, False), (4, False), (4, True)}
+    assert {split_of_k(K) for K in FEW_ROW_K} == every
+    assert {split_of_k(K) for K in FEW_ROW_K if K % 128} == every  # with a part window too
+    assert {split_of_k(16 * c) for c in range(1, 8192)} == every   # there are no others
