@@ -100,3 +100,30 @@ def test_more_tokens_than_a_launch_has_threads_for():
     # fp64 scores, then one rounding to fp32
     assert bool(((w[:, 0].double() - ref).abs() <= 1.0001 * o.U * ref).all())
     check_tables(ids, E, off, perm, rows, sop)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("score,biased,lead,renorm", [("softmax", False, 1, False), ("softmax", True, 2, True),
+                                                      ("sigmoid", True, 2, True), ("sigmoid", False, 1, False)])
+def test_long_grouped_batches(dtype, score, biased, lead, renorm):
+    """20011 tokens, 3 of 8 groups of 20 experts: ids, weights and tables against fp64 on the device."""
+    T, E, k, n, keep, scale = 20011, 160, 6, 8, 3, 16.0
+    gen = torch.Generator(device=cuda()).manual_seed(41)
+    x = (1.5 * torch.randn(T, E, device=cuda(), generator=gen)).to(dtype)
+    bias = 0.05 * torch.randn(E, device=cuda(), generator=gen) if biased else None
+    ids, w, off, perm, rows, sop = w4mod().moe_route_scored(x, k, bias=bias, score=score, n_groups=n, topk_groups=keep,
+                                                            group_lead=lead, renorm=renorm, scale=scale)
+    xd = x.double()
+    s = torch.sigmoid(xd) if score == "sigmoid" else torch.softmax(xd, 1)
+    v = s + bias.double() if biased else s
+    value = torch.sort(v.view(T, n, E // n), dim=2, descending=True).values[:, :, :lead].sum(2)
+    kept = torch.sort(value, dim=1, descending=True, stable=True).indices[:, :keep]
+    open_ = torch.zeros(T, n, dtype=torch.bool, device=cuda()).scatter_(1, kept, True).repeat_interleave(E // n, 1)
+    key = torch.where(open_, v if biased else xd, -float("inf"))
+    want = torch.sort(key, dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(ids.long(), want)
+    ref = s.gather(1, want)
+    ref = scale * (ref / ref.sum(1, keepdim=True) if renorm else ref)
+    # fp64 scores and sums (a few 1e-16), then one rounding to fp32
+    assert bool(((w.double() - ref).abs() <= 1.0001 * o.U * ref).all())
+    check_tables(ids, E, off, perm, rows, sop)
