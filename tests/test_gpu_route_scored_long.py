@@ -1,12 +1,12 @@
 """GPU tests of the scored router over very long batches and hot experts: the tables against sorting on the device,
-the weights against fp64, and the time per pair."""
+the weights against fp64, the time per pair, and the layer of 4-bit experts behind the router."""
 from __future__ import annotations
 
 import numpy as np
 import pytest
 
 from tests import w8_oracle as o
-from tests.gpu_common import cuda, to_host
+from tests.gpu_common import cuda, to_dev, to_host
 
 pytestmark = pytest.mark.gpu
 
@@ -127,3 +127,50 @@ def test_long_grouped_batches(dtype, score, biased, lead, renorm):
     # fp64 scores and sums (a few 1e-16), then one rounding to fp32
     assert bool(((w.double() - ref).abs() <= 1.0001 * o.U * ref).all())
     check_tables(ids, E, off, perm, rows, sop)
+
+
+@pytest.mark.parametrize("T", [1, 37, 300])
+def test_layer_of_4_bit_experts(orc, T):
+    """Scored router -> quantizer -> gate/up product -> SiLU requant -> down product -> combine with the 4-bit expert
+    product, the shared expert as index E; each stage against the oracle on the stage's own inputs."""
+    w4 = w4mod()
+    rng = np.random.default_rng(T)
+    E, k, H, I = 6, 3, 256, 256
+    x = rng.standard_normal((T, H)).astype(np.float32)
+    logits = rng.standard_normal((T, E)).astype(np.float32)
+    bias = (0.1 * rng.standard_normal(E)).astype(np.float32)
+
+    def experts(N, K):
+        per = [orc.quantize_weights((0.05 * rng.standard_normal((N, K))).astype(np.float32)) for _ in range(E + 1)]
+        packed = np.stack([orc.pack_nibbles(q) for q, _, _ in per])
+        return per, [to_dev(packed)] + [to_dev(np.stack([p[i] for p in per]).view(np.int16)) for i in (1, 2)]
+
+    gate_up, gd = experts(2 * I, H)
+    down, dd = experts(H, I)
+    cfg = dict(score="sigmoid", n_groups=3, topk_groups=2, group_lead=2, renorm=True, scale=2.5)
+    ids, w, off, _, rows, sop = w4.moe_route_scored(to_dev(logits), k, bias=to_dev(bias), with_shared=True, **cfg)
+    S = T * k + T
+    qa, sa = w4.quantize_act(to_dev(x))
+    gu = w4.moe_grouped_gemm(qa, sa, rows, off, *gd, max_slots=S)
+    qh, hs = w4.silu_mul_quantize(gu)
+    y = w4.moe_grouped_gemm(qh, hs, None, off, *dd, max_slots=S)
+    out = w4.moe_combine(y, sop, w, y_shared=y[T * k:])
+
+    ids_r, w_r = o.route(logits, k, bias=bias, **cfg)
+    off_r, _, rows_r, sop_r = o.tables(ids_r, E, True)
+    assert np.array_equal(to_host(ids), ids_r) and np.array_equal(to_host(off), off_r)
+    assert np.array_equal(to_host(rows), rows_r) and np.array_equal(to_host(sop), sop_r)
+    for e in range(E + 1):
+        s = slice(off_r[e], off_r[e + 1])
+        if s.start == s.stop:
+            continue
+        for got, a, a_scale, per in ((gu, to_host(qa)[rows_r[s]], to_host(sa)[rows_r[s]], gate_up),
+                                     (y, to_host(qh)[s], to_host(hs)[s], down)):
+            ref, mag = orc.gemm(a, a_scale, *per[e])
+            assert (np.abs(to_host(got)[s].astype(np.float64) - ref) <= 1e-5 * mag + 1e-6).all(), e
+    yh = to_host(y).astype(np.float64)
+    terms = to_host(w).astype(np.float64)[:, :, None] * yh[sop_r.reshape(T, k)]
+    ref = terms.sum(1) + yh[T * k:]
+    # k fused multiply-adds and one addition: each rounds a partial sum of at most the magnitudes' sum
+    bound = (k + 1) * 1.001 * o.U * (np.abs(terms).sum(1) + np.abs(yh[T * k:]))
+    o.close(to_host(out), ref, bound, 0.0, 0.0)
