@@ -334,8 +334,10 @@ w4a8_status w4a8_moe_route(const float *logits, int64_t T, int32_t E, int32_t to
  *         fp64 ends) or the softmax of the token's logits (W4A8_SCORE_SOFTMAX); 0
  *         where x is -inf
  *   v   = s + bias[e], or s without a bias; the picks' order goes by key = v, or by x
- *         itself without a bias.  bias: fp32 [E] or NULL, NaN counting as -inf.  An
- *         expert whose logit or bias is -inf has v = key = -inf
+ *         itself without a bias, which tells experts apart whose scores are the same
+ *         fp64 number (with a bias such a tie goes to the lower id, and groups are
+ *         compared by v in both).  bias: fp32 [E] or NULL, NaN and large values
+ *         counting as for x.  An expert whose logit or bias is -inf has v = key = -inf
  *   the E experts form n_groups runs of E / n_groups; a group's value is the sum of
  *         its group_lead (1 or 2) largest v, and only the topk_groups groups of the
  *         largest values stay (ties: the lower group).  n_groups = 1 takes all

@@ -17,7 +17,7 @@
 //
 // A few MB at most are read and written; the time is latency and instructions.  E 384, k 8,
 // sigmoid + bias: one token 6.5 us (one launch), 4096 tokens 11 us here and 13 us in the placing;
-// 20011 tokens, E 160, softmax in 8 groups: 27 + 20 us (every VALU cycle used).
+// 20011 tokens, E 160, softmax in 8 groups: 27 + 21 us.
 #include <type_traits>
 
 #include "w8_internal.hpp"
@@ -38,13 +38,13 @@ __device__ __forceinline__ float logit_at(const __bf16 *p, int64_t i) { return (
 __device__ __forceinline__ float tame(float x) { return x > -INFINITY ? fminf(x, 3.402823466e38f) : -INFINITY; }
 
 // e^d for d <= 709 (-inf: 0) in fp64: d = n ln 2 + r with |r| <= ln 2 / 2, the Taylor series of e^r to
-// r^13 (the rest is below 2^-59) and a scaling by 2^n.  About 20 instructions, where the library's
-// form with its special cases takes some 40, and a token needs one for each expert.
+// r^13 (the rest is below 2^-57 of e^r) and a scaling by 2^n.  About 20 instructions, where the
+// library's form with its special cases takes some 40, and a token needs one for each expert.
 __device__ __forceinline__ double exp64(double d) {
     d = fmax(d, -1100.0);  // 2^-1587 and below: 0
     const double n = __builtin_rint(d * 1.4426950408889634);
-    // ln 2 in two parts, the first with 21 trailing zero bits: n times it is exact
-    const double r = fma(n, -1.9082149292705877e-10, fma(n, -0.693147180369123816490, d));
+    // Cody and Waite's reduction: ln 2 cut to its first 32 bits, which n times are exact, and the rest
+    const double r = fma(n, -0x1.a39ef35793c76p-33, fma(n, -0x1.62e42feep-1, d));
     double p = 1.0 / 6227020800.0;
     p = fma(p, r, 1.0 / 479001600.0);
     p = fma(p, r, 1.0 / 39916800.0);
@@ -286,8 +286,9 @@ __global__ __launch_bounds__(kRouteThreads) void route_scored_kernel(const L *__
 // Expert buckets: workgroup e places the pairs of expert e, in increasing pair index, behind the
 // pairs of all lower experts.  Each wave owns a contiguous run of pairs and reads it twice (to count,
 // then to place), 256 pairs at a time, four neighbours per lane, counting with ballots.  The ids
-// come from L2, E times over, which for some 10^5 pairs costs less than a scan over chunks with
-// its extra launches.  32768 pairs, E 384: 12.7 us (71 with a contiguous run of pairs per thread).
+// come from L2, E times over, and that is the time: 32768 pairs, E 384 12.8 us (71 with a contiguous
+// run of pairs per thread).  A count per chunk and a scan over the chunks, which would read them
+// twice in all, has not been measured.
 // shared_T >= 0: a shared expert with that many slots follows.
 typedef int32_t ids4 __attribute__((ext_vector_type(4), aligned(4)));
 template <int THREADS>
