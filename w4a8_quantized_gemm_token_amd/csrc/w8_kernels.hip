@@ -10,9 +10,10 @@
 //
 // Two loops.  Up to 16 rows (slice_walk) the weights are read once and are the whole cost: 235 MB
 // in 39.7 us (K 8192, N 28672, one row), 5.9 TB/s, where a large copy moves 5.1 TB/s.  More rows go
-// through LDS tiles (tile_unit): 4096 x 8192 x 8192 in 199-218 us on different boxes, 2.5-2.8 POPS;
-// the matrix pipes alone, fed from registers with such codes, ran at 3.9 POPS (the clock drops to
-// 1.9 GHz under them).
+// through LDS tiles (tile_unit): 4096 x 8192 x 8192 in 199-218 us among other passes on different
+// boxes, 2.5-2.8 POPS, and from 203 us up to 239 in the median of 20 launches in a row, as the clock
+// falls under the load; the matrix pipes alone, fed from registers, run at 3.9 POPS with random codes
+// and at 4.8 with zeros.
 #include <algorithm>
 #include <type_traits>
 
@@ -48,11 +49,9 @@ __device__ __forceinline__ int64_t clamp_slots(int64_t v, int64_t max_slots) {
 // before it is multiplied, so the one barrier per stage stands between the halves of stage g:
 // there every wave holds the fragments of its second half in registers (the stage's buffer is
 // free for stage g + NST) and stage g + 1 has landed (its first half may be read).
-// Measured on 256 x 256, M 4096, K = N 8192 (MFMA busy 76% of the CUs' busy cycles, no LDS bank
-// conflicts, 20% of the L2 reads miss): without the loads 164 us, without the LDS reads 231, with
-// every line in L2 189.  Not kept: stages of 64 bytes, five of them (237 us: twice the barriers, half
-// lines from L2); four waves of 128 x 128 (229); two 128 x 256 workgroups of four waves per CU
-// (279); 32x32x32 products (266); raised wave priority around the products (231).
+// 256 x 256 at M 4096, K = N 8192: MFMA busy 77% of the CUs' busy cycles, no LDS bank conflicts, 20% of
+// the L2 reads miss.  The other forms take 249 us there (128 x 256), 320 (128 x 128), 447 (64 x 64) and
+// 598 (32 x 64), this one 214.
 typedef __attribute__((address_space(3))) void *lds_ptr_t;
 typedef const __attribute__((address_space(1))) void *glb_ptr_t;
 
@@ -92,9 +91,9 @@ struct Deal {
 };
 
 // src_row(r), r < rows: activation row of the tile's row r, or -1 (computed as row 0, not stored).
-// WIDE: rows may lie 2^32 bytes or more behind qa.  (Its
-// loads take 64-bit addresses, and the compiler counts those as able to touch LDS by themselves:
-// it then waits for every access in flight where it would wait for some.)
+// WIDE: rows may lie 2^32 bytes or more behind qa.  (Its loads take 64-bit addresses, and the compiler
+// counts those as able to touch LDS by themselves: it then waits for every access in flight where
+// it would wait for some.)
 template <typename C, bool WIDE, typename T, typename SrcRow>
 __device__ __forceinline__ void tile_unit(uint8_t *lds, const int8_t *__restrict__ qa,
                                           const float *__restrict__ a_scale, SrcRow src_row, int64_t slot0, int rows,
@@ -190,7 +189,7 @@ __device__ __forceinline__ void tile_unit(uint8_t *lds, const int8_t *__restrict
     // half ks, if rd) and after every second one a load of stage g into the buffer sti (if ld), in
     // just this order: the reads are then back long before the half ends, and no burst of loads
     // holds up the products.  (The compiler's own order put the reads behind the loads, at the end:
-    // 218 us against 210 at M 4096, K = N 8192.)
+    // 225 us against 211 at M 4096, K = N 8192.)
     auto half = [&](const Frags &now, auto rd, Frags &then, int st, int ks, auto ld, int g, int sti) {
         // read r and load d follow these products (a small tile has fewer products than reads or loads)
         constexpr auto read_at = [](int r) { return kMul > kReads + 2 ? r + 2 : r * kMul / kReads; };
@@ -343,7 +342,7 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 256 ? 2 : 1) void gemm_
 // Channels past N and bytes past the array read as 0 (the descriptor ends with the array); k past
 // K and the windows that a wave has no share of are zeros on the activations' side.
 // K 8192, N 28672: one row 39.7 us, 16 rows 42.6 (49.5 and 76 with the rows read from the caches per
-// window and one tile per workgroup; 56 and 60 with a ring of 8 windows, which spills).
+// window and one tile per workgroup).
 template <int BANKS>
 __device__ __forceinline__ v4i ror8_into(v4i old, v4i src) {
     v4i r;
@@ -444,7 +443,7 @@ __device__ __forceinline__ void slice_walk(v4i (*red)[kMaxSliceWaves][64], Walk 
                 }
                 if (ONE || ++pass == passes) {
                     pass = 0;
-red[turn][wave][lane] = acc;
+                    red[turn][wave][lane] = acc;
                     // LDS done, the weights stay in flight; the other half of red was read before this
                     // barrier by the wave that ended the tile before
                     __asm__ volatile("" ::: "memory");
@@ -611,8 +610,8 @@ struct ExpertWalk {
 };
 
 // Experts of up to 16 slots: a workgroup's run of tiles goes through one expert after the other.
-// Bound by the weights: 64 tokens, top 8 of 384, K 7168, N 4096 (6.4 GB) 0.95 ms here, 1.05 ms on
-// persistent 32 x 64 tiles; one token 44 us.
+// Bound by the weights: 64 tokens, top 8 of 384, K 7168, N 4096 (212-220 experts, 6.2-6.5 GB) 0.96 ms here
+// (1.69 ms when every 16-channel tile read its rows and shared out k by itself); one token 45 us.
 template <int NW, bool ONE>
 __global__ __launch_bounds__(64 * kMaxSliceWaves) void grouped_w8a8_slice_kernel(
     const int8_t *__restrict__ qa, const float *__restrict__ a_scale, int64_t R, const int32_t *__restrict__ row_index,
@@ -632,10 +631,10 @@ __global__ __launch_bounds__(64 * kMaxSliceWaves) void grouped_w8a8_slice_kernel
 
 // Experts with more than lo slots on C's tiles: a persistent grid over (row block, column tile)
 // units, an expert's row blocks next to each other on one XCD, so that its weights come
-// through one L2.  4096 tokens, top 8 of 384, K 7168, N 4096 (338 experts here, 10 GB) 2.13 ms: 4.9
-// TB/s of weights with 62% of the products' time behind them.  A 64 x 256 form for 17-64 slots and this
-// one for the rest took as long (0.91 + 1.23 ms) with a launch more, 256 x 256 above 128 slots 5%
-// longer, two stages instead of three 12%, loads that warm L2 ahead 17%.
+// through one L2.  4096 tokens, top 8 of 384, K 7168, N 4096 (some 335 experts here, 10 GB) 2.13 ms: 4.9
+// TB/s of weights, MFMA busy 42% of the CUs' busy cycles.  A 64 x 256 form for 17-64 slots and this one
+// for the rest took as long (0.91 + 1.23 ms) with a launch more, 256 x 256 above 128 slots 5% longer, two
+// stages instead of three 12%.
 template <typename C>
 __global__ __launch_bounds__(C::kThreads) void grouped_w8a8_tile_kernel(
     const int8_t *__restrict__ qa, const float *__restrict__ a_scale, int64_t R, const int32_t *__restrict__ row_index,
@@ -734,16 +733,22 @@ static hipError_t gemm_w8a8_typed(const int8_t *qa, const float *a_scale, int64_
                                   const float *w_scale, int64_t N, const float *bias, T *out, int64_t ldo,
                                   hipStream_t stream) {
     // Few rows and a long k, or runs of at least four 16-channel tiles for every workgroup: k shared
-    // out within the workgroup (K 16384, N 4096, one row: 18.7 us against 24.3 on 32 x 64 tiles;
-    // K 4096, N 14336: 17.7 against 14.3).
+    // out within the workgroup.  us with weights from memory, this loop / 32 x 64 tiles, one row: K 8192,
+    // N 28672 40.4 / 43.8; K 8192, N 16384 26.2 / 29.6; K 16384, N 4096 19.1 / 24.6; on the tiles' side
+    // K 8192, N 8192 17.2 / 16.3 and K 4096, N 14336 17.3 / 15.0.  The border follows N and K one at a
+    // time and is not the best everywhere: N from 16384 on with K up to 2048 would be faster on tiles (K
+    // 2048, N 28672 19.3 / 12.9), K 7168 and 8192 with N up to 4096 here (K 8192, N 4096 11.3 / 14.5),
+    // and 16 rows of K 16384 from N 6144 on, in two passes, on tiles (N 28672 108 / 86.9).
     if (M <= 16 && (K > 8192 || N >= 16 * 4 * kCus))
         return launch_slice(qa, a_scale, M, K, qw, w_scale, N, bias, out, ldo, stream);
     // Else the tile form of the least expected time.  Per 256 tiles (one for every CU) and K 8192 the
     // forms take about 100 us (256 x 256), 60 (128 x 256), 39 (128 x 128), 15.5 (64 x 64, and 5 once) and
     // 10.7 (32 x 64, and 8 once), part rounds as whole ones: large tiles read less per product, small
-    // ones leave fewer CUs idle.  Measured against the other forms: M 512, K = N 8192 128 x 128 41 us
-    // (128 x 256 58, 64 x 64 68); M 77, K 4112, N 5003 32 x 64 10 us (64 x 64 14, 128 x 128 22); M 256, K 8192,
-    // N 28672 128 x 256 74 us (128 x 128 87, 256 x 256 106).
+    // ones leave fewer CUs idle.  Over 141 sizes of M 17-4096, K 512-8192, N 2048-28672 the form of this
+    // rule is within 9% of the fastest one (at short K too, where the constants do not scale with it).
+    // us against the other forms: M 512, K = N 8192 128 x 128 43 (128 x 256 60, 64 x 64 71); M 77, K 4112,
+    // N 5003 32 x 64 12.5 (64 x 64 13.0, 128 x 128 30); M 256, K 8192, N 28672 128 x 256 76 (128 x 128 90,
+    // 256 x 256 110); the widest miss M 192, K = N 8192 64 x 64 39 (128 x 128 36).
     auto cost = [&](int64_t bm, int64_t bn, double round, double once) {
         const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
         return (double)((tiles + kCus - 1) / kCus) * round + once;
