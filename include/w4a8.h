@@ -75,7 +75,7 @@ typedef enum {
     W4A8_EWORKSPACE = 4     /* the caller's workspace is smaller than the call needs */
 } w4a8_status;
 
-#define W4A8_ABI_VERSION 7
+#define W4A8_ABI_VERSION 8
 #define W4A8_GROUP 128
 
 /* Element types of the entry points that take more than fp32. */
@@ -300,6 +300,80 @@ w4a8_status w4a8_moe_grouped_gemm_w8a8(const int8_t *qa, const float *a_scale, i
                                        const int32_t *row_index, const int32_t *expert_offsets,
                                        int32_t E, int64_t K, const int8_t *qw, const float *w_scale,
                                        int64_t N, int64_t max_slots, float *out, hipStream_t stream);
+
+/* ------------------------------------------- low-rank adapters of many requests
+ * A shared projection whose requests each bring a low-rank term of their own
+ * (B_a A_a beside the quantized W): one call adds every row's term to the output that
+ * w4a8_gemm, w4a8_gemm_w8a8 or any other product has left. */
+
+/* Device.  With a = row_adapter[m] and rank_a = min(ranks[a], R) (R without ranks, 0 for a
+ * negative entry):
+ *     v_j       = sum_k x[m][k] * A[a][j][k]                          j < rank_a
+ *     out[m][n] = T(base[m][n] + scale[a] * sum_j v_j * B[a][n][j])   T by out_type
+ * in fp32 with one rounding to T; a row whose a is outside [0, L) has no adapter, and
+ * out[m] = base[m].  Rows may come in any order of adapters; rows of one adapter that stand
+ * within 64 rows of each other share its weights' loads.
+ *   x [M][K] of x_type (row stride ldx elements), A [L][R][K] and B [L][N][R] of ab_type
+ *   (W4A8_F16 or W4A8_BF16), row_adapter int32 [M], ranks int32 [L] or NULL, scale fp32 [L]
+ *   or NULL (1), base and out [M][N] of out_type (row strides ldb, ldo; the elements between
+ *   rows are not written).  base may be out itself (the same pointer and stride: the term is
+ *   added in place and rows without an adapter are not touched); otherwise the two do not
+ *   overlap.  Entries of A and B past rank_a are not used, whatever they hold.
+ * How exactly the two products take part: x and v enter the matrix cores as sums of 16-bit
+ * values that together hold at least 22 bits of each with out_type W4A8_F32 and 16 with the
+ * 16-bit types; everything is accumulated in fp32.  Infinities and NaN reach the outputs of
+ * their own row (x) or column (B) or adapter (A) only.
+ * Any M >= 0 and N in [1, 2^23]; K a positive multiple of 8 up to 2^20; R a multiple of 8 in
+ * [8, 256]; 1 <= L <= 65536.  A, B and workspace 16-byte aligned, x, base and out aligned to
+ * their element.  workspace: device memory of at least w4a8_lora_workspace_size(M, K, L, R)
+ * bytes; its contents need not be set or kept, and calls that may overlap (other streams,
+ * graphs replayed side by side) need one each.
+ * Errors: W4A8_EINVAL (null, bad sizes, strides or alignment), W4A8_EUNSUPPORTED (another
+ * type), W4A8_EWORKSPACE.  M == 0 is a no-op. */
+size_t      w4a8_lora_workspace_size(int64_t M, int64_t K, int32_t L, int32_t R);
+w4a8_status w4a8_lora_add(const void *x, int32_t x_type, int64_t ldx, int64_t M, int64_t K,
+                          const int32_t *row_adapter, const void *A, const void *B, int32_t ab_type, int32_t L,
+                          int32_t R, const int32_t *ranks, const float *scale, const void *base, int64_t ldb,
+                          int64_t N, void *out, int32_t out_type, int64_t ldo, void *workspace, size_t ws_bytes,
+                          hipStream_t stream);
+
+/* ------------------------------------------------- between two blocks of a model */
+
+/* Device.  What stands between a block's output y and the next block's products, per row m:
+ *     p      = post(y[m]) (or y[m] with W4A8_NORM_NONE)
+ *     r'     = S(res_scale * res[m] + y_scale * gate * p)          S by res_type
+ *     z      = pre(r') of the r' that is stored (or r' with W4A8_NORM_NONE)
+ *     res_out[m] = r',  z_out[m] = Z(z)
+ *     a_scale[m] = s = max_h |fp32(z)| * fp32(1/127),  qa[m] = clamp(rint(fp32(z) / s), -127, 127)
+ * with RMS(u) = u / sqrt(mean(u^2) + eps) * w + b and LAYER(u) = RMS of u - mean(u) (w NULL: 1,
+ * b NULL: 0).  Everything up to z is taken in fp64, so that codes do not turn on the order of
+ * fp32 sums; each output is rounded to fp32 and from there to its type (values past a 16-bit
+ * type's range become infinities).  The scale is a product, as tensor code on this device forms
+ * max / 127, so that the codes are those of the unfused steps bit for bit; w4a8_quantize_act's
+ * quotient is within one fp32 step of it.  A row with s == 0 gets codes 0.
+ *   res, y, gate, z_out: rows of res_type, y_type, gate_type, z_type with strides ldr, ldy,
+ *   ldg, ldz; res_out of res_type, stride ldro.  The elements between rows are not written.
+ *   res NULL: 0.  y NULL: no block before (r' = S(res_scale * res); post is then NONE and gate
+ *   NULL).  gate NULL: 1; ldg = 0: one gate vector [H] for all rows.  res_out, z_out and the
+ *   pair qa [M][H], a_scale [M] may each be NULL, not all.  post_w, post_b, pre_w, pre_b:
+ *   fp32 [H] or NULL.
+ *   An output may be an input itself (the same pointer, type and stride: the stream updated in
+ *   place); otherwise outputs overlap nothing.
+ * Any M >= 0, 1 <= H <= 32768.  res, y, gate, res_out and z_out aligned to their element, qa
+ * 16-byte aligned.  eps positive, the scales finite.  A row whose z is not finite gets
+ * unspecified codes, as in w4a8_quantize_act; other rows are not affected.
+ * Errors: W4A8_EINVAL (null, bad sizes, strides, alignment or values), W4A8_EUNSUPPORTED
+ * (another type or norm).  M == 0 is a no-op. */
+#define W4A8_NORM_NONE 0
+#define W4A8_NORM_RMS 1
+#define W4A8_NORM_LAYER 2
+w4a8_status w4a8_residual_norm_quantize(const void *res, int32_t res_type, int64_t ldr, const void *y, int32_t y_type,
+                                        int64_t ldy, int64_t M, int64_t H, int32_t post, const float *post_w,
+                                        const float *post_b, const void *gate, int32_t gate_type, int64_t ldg,
+                                        double res_scale, double y_scale, void *res_out, int64_t ldro, int32_t pre,
+                                        const float *pre_w, const float *pre_b, double eps, void *z_out,
+                                        int32_t z_type, int64_t ldz, int8_t *qa, float *a_scale,
+                                        hipStream_t stream);
 
 /* ---------------------------------------------------------------------- MoE */
 

@@ -16,7 +16,7 @@ import os
 import numpy as np
 
 GROUP = 128
-ABI_VERSION = 7          # W4A8_ABI_VERSION of the header this binding follows
+ABI_VERSION = 8          # W4A8_ABI_VERSION of the header this binding follows
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libw4a8.so")
 
@@ -28,6 +28,7 @@ EXPORTS = (
     "w4a8_tm_bytes", "w4a8_weights_to_tm", "w4a8_gemm_tm",
     "w4a8_channel_absmax", "w4a8_smooth_factors", "w4a8_pack_weights_device_smooth", "w4a8_quantize_act_smooth",
     "w4a8_gemm_w8a8", "w4a8_moe_grouped_gemm_w8a8", "w4a8_moe_route_scored",
+    "w4a8_lora_workspace_size", "w4a8_lora_add", "w4a8_residual_norm_quantize",
     "w4a8_moe_route", "w4a8_moe_grouped_gemm", "w4a8_moe_grouped_gemm_debug_isums", "w4a8_silu_mul_quantize",
     "w4a8_moe_combine",
     "w4a8_moe_ffn_workspace_size", "w4a8_moe_ffn_workspace_layout", "w4a8_moe_ffn",
@@ -55,7 +56,7 @@ def load() -> ctypes.CDLL:
         raise ImportError(f"{LIB_PATH} is missing: build it with "
                           "`python w4a8_quantized_gemm_token_amd/build.py` (no CPU fallback exists)")
     lib = ctypes.CDLL(LIB_PATH)
-    p, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+    p, i64, i32, sz, f64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_double
     sig = {
         "w4a8_abi_version": (ctypes.c_int, []),
         "w4a8_status_str": (ctypes.c_char_p, [ctypes.c_int]),
@@ -80,6 +81,11 @@ def load() -> ctypes.CDLL:
                                                  ctypes.c_float, p, p, p, p, p, p, p]),
         "w4a8_gemm_w8a8": (ctypes.c_int, [p, p, i64, i64, p, p, i64, p, p, i32, i64, p]),
         "w4a8_moe_grouped_gemm_w8a8": (ctypes.c_int, [p, p, i64, p, p, i32, i64, p, p, i64, i64, p, p]),
+        "w4a8_lora_workspace_size": (sz, [i64, i64, i32, i32]),
+        "w4a8_lora_add": (ctypes.c_int, [p, i32, i64, i64, i64, p, p, p, i32, i32, i32, p, p, p, i64, i64, p, i32, i64,
+                                         p, sz, p]),
+        "w4a8_residual_norm_quantize": (ctypes.c_int, [p, i32, i64, p, i32, i64, i64, i64, i32, p, p, p, i32, i64, f64,
+                                                       f64, p, i64, i32, p, p, f64, p, i32, i64, p, p, p]),
         "w4a8_moe_grouped_gemm": (ctypes.c_int, [p, p, i64, p, p, i32, i64, p, p, p, i64, i32, i64, p, p]),
         "w4a8_moe_grouped_gemm_debug_isums": (ctypes.c_int, [p, i64, p, p, i32, i64, p, p, i64, i32, i64, p, p]),
         "w4a8_silu_mul_quantize": (ctypes.c_int, [p, i64, i64, p, p, p, p]),
@@ -434,6 +440,122 @@ def linear(x, packed, scale, zp, path: int = 0):
     """Quantize x per token and run the W4A8 product: float32 [M][N]."""
     qa, sc = quantize_act(x)
     return gemm(qa, sc, packed, scale, zp, path=path)
+
+
+# ----------------------------------------------------------------- adapters, between blocks
+def _ld(t, rows: int, width: int) -> int:
+    return t.stride(0) if rows > 1 else max(width, 1)
+
+
+def lora_workspace(M: int, K: int, L: int, R: int) -> int:
+    """Bytes of the workspace of lora_add (0 for sizes that it does not take)."""
+    return int(load().w4a8_lora_workspace_size(M, K, L, R))
+
+
+def _lora_args(out, x, row_adapter, A, B, workspace, scale, ranks, base):
+    torch = _torch()
+    M, K = x.shape
+    L, R = A.shape[0], A.shape[1]
+    N = B.shape[1]
+    base = out if base is None else base
+    _is(A, (L, R, K), A.dtype, "A")
+    _is(B, (L, N, R), A.dtype, "B")
+    _is(row_adapter, (M,), torch.int32, "row_adapter")
+    _is(ranks, (L,), torch.int32, "ranks")
+    _is(scale, (L,), torch.float32, "scale")
+    assert tuple(out.shape) == (M, N), "out: [M][N] expected"
+    _is(base, (M, N), out.dtype, "base")
+    _is(workspace, (workspace.numel(),), torch.uint8, "workspace")
+    _same_device(out, x, row_adapter, A, B, workspace, scale, ranks, base)
+    return (_dev_rows_ptr(x), _dtype_code(x.dtype), _ld(x, M, K), M, K, _dev_ptr(row_adapter), _dev_ptr(A), _dev_ptr(B),
+            _dtype_code(A.dtype), L, R, _dev_ptr(ranks), _dev_ptr(scale), _dev_rows_ptr(base), _ld(base, M, N), N,
+            _dev_rows_ptr(out), _dtype_code(out.dtype), _ld(out, M, N), _dev_ptr(workspace), workspace.numel(),
+            _stream(x.device))
+
+
+def lora_add(out, x, row_adapter, A, B, workspace=None, scale=None, ranks=None, base=None):
+    """out[m] = base[m] + scale[a] B[a] (A[a] x[m]) with a = row_adapter[m]: the low-rank term of each row's adapter
+    beside a shared projection.  out [M][N] (base None: added in place), x [M][K], row_adapter int32 [M] (rows outside
+    [0, L) have none), A [L][R][K] and B [L][N][R] float16 or bfloat16, scale float32 [L], ranks int32 [L] (how many of
+    an adapter's R rows count).  x, out and base may have strided rows.  Returns out."""
+    torch = _torch()
+    with torch.cuda.device(x.device):
+        if workspace is None:
+            workspace = _empty((lora_workspace(x.shape[0], x.shape[1], A.shape[0], A.shape[1]),), torch.uint8, x)
+        _call("w4a8_lora_add", *_lora_args(out, x, row_adapter, A, B, workspace, scale, ranks, base))
+    return out
+
+
+def prepare_lora_add(out, x, row_adapter, A, B, workspace, scale=None, ranks=None, base=None) -> Launch:
+    """Prepared w4a8_lora_add; workspace: uint8 [lora_workspace(M, K, L, R)] or more, of this call alone while it
+    may run."""
+    return Launch("w4a8_lora_add", _lora_args(out, x, row_adapter, A, B, workspace, scale, ranks, base),
+                  (out, x, row_adapter, A, B, workspace, scale, ranks, base))
+
+
+NORMS = {"none": 0, "rms": 1, "layer": 2}  # W4A8_NORM_*
+
+
+def _norm_args(res, y, outs, post, post_w, post_b, gate, res_scale, y_scale, pre, pre_w, pre_b, eps):
+    torch = _torch()
+    res_out, z, qa, a_scale = outs
+    like = res if res is not None else y
+    M, H = like.shape
+    assert post in NORMS and pre in NORMS, f"norm: one of {sorted(NORMS)} expected"
+    stream_type = res.dtype if res is not None else res_out.dtype if res_out is not None else torch.float32
+    _is(y, (M, H), None if y is None else y.dtype, "y")
+    _is(res_out, (M, H), stream_type, "res_out")
+    _is(z, (M, H), None if z is None else z.dtype, "z")
+    _is(qa, (M, H), torch.int8, "qa")
+    _is(a_scale, (M,), torch.float32, "a_scale")
+    for w, what in ((post_w, "post_w"), (post_b, "post_b"), (pre_w, "pre_w"), (pre_b, "pre_b")):
+        _is(w, (H,), torch.float32, what)
+    assert gate is None or tuple(gate.shape) in ((H,), (M, H)), "gate: [H] or [M][H] expected"
+    _same_device(res, y, *outs, post_w, post_b, gate, pre_w, pre_b)
+
+    def rows(t):
+        return (None, 0, 0) if t is None else (_dev_rows_ptr(t), _dtype_code(t.dtype), _ld(t, M, H))
+
+    if gate is not None and gate.dim() == 1:
+        gates = (_dev_ptr(gate), _dtype_code(gate.dtype), 0)
+    else:
+        gates = rows(gate)
+    r, o, zs = rows(res), rows(res_out), rows(z)
+    return (r[0], _dtype_code(stream_type), r[2], *rows(y), M, H, NORMS[post], _dev_ptr(post_w), _dev_ptr(post_b), *gates,
+            float(res_scale), float(y_scale), o[0], o[2], NORMS[pre], _dev_ptr(pre_w), _dev_ptr(pre_b), float(eps), *zs,
+            _dev_ptr(qa), _dev_ptr(a_scale), _stream(like.device))
+
+
+def residual_norm_quantize(res, y=None, post: str = "none", post_w=None, post_b=None, gate=None, res_scale: float = 1.0,
+                           y_scale: float = 1.0, pre: str = "rms", pre_w=None, pre_b=None, eps: float = 1e-6,
+                           res_out=None, z_dtype=None, quantize: bool = True):
+    """Between two blocks: stream = res_scale * res + y_scale * gate * post(y), z = pre(stream), and z's INT8 codes with a
+    scale per row.  res and y [M][H] float32, float16 or bfloat16 (either may be None), gate
+    [H] or [M][H], norm weights and biases float32 [H]; norms "none", "rms" or "layer".  Rows may be strided.  res_out:
+    where the stream goes (a new tensor if None, of res's type; pass res itself to update it in place).
+    Returns (stream, z or None, qa or None, a_scale or None); z is written if z_dtype is given."""
+    torch = _torch()
+    like = res if res is not None else y
+    M, H = like.shape
+    if res_out is None:
+        res_out = _empty((M, H), like.dtype, like)
+    z = None if z_dtype is None else _empty((M, H), z_dtype, like)
+    qa, a_scale = (_empty((M, H), torch.int8, like), _empty((M,), torch.float32, like)) if quantize else (None, None)
+    outs = (res_out, z, qa, a_scale)
+    with torch.cuda.device(like.device):
+        _call("w4a8_residual_norm_quantize", *_norm_args(res, y, outs, post, post_w, post_b, gate, res_scale, y_scale, pre,
+                                                         pre_w, pre_b, eps))
+    return outs
+
+
+def prepare_residual_norm_quantize(res, y, outs, post: str = "none", post_w=None, post_b=None, gate=None,
+                                   res_scale: float = 1.0, y_scale: float = 1.0, pre: str = "rms", pre_w=None, pre_b=None,
+                                   eps: float = 1e-6) -> Launch:
+    """Prepared w4a8_residual_norm_quantize into outs = (stream, z, qa, a_scale), each of which may be None (qa and
+    a_scale together)."""
+    return Launch("w4a8_residual_norm_quantize", _norm_args(res, y, outs, post, post_w, post_b, gate, res_scale, y_scale,
+                                                            pre, pre_w, pre_b, eps),
+                  (res, y, post_w, post_b, gate, pre_w, pre_b) + tuple(outs))
 
 
 # ----------------------------------------------------------------- MoE

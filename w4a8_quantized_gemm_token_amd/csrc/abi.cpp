@@ -15,6 +15,7 @@
 #include <thread>
 #include <vector>
 
+#include "block_internal.hpp"
 #include "w8_internal.hpp"
 
 namespace w4a8 {
@@ -497,6 +498,102 @@ w4a8_status w4a8_moe_grouped_gemm_w8a8(const int8_t *qa, const float *a_scale, i
     return hip_status(launch_grouped_gemm_w8a8(qa, a_scale, R, row_index, expert_offsets, E, K, qw, w_scale, N,
                                                max_slots, out, stream),
                       "grouped_gemm_w8a8 launch");
+}
+
+// ------------------------------------------------------------------ adapters, between blocks
+namespace {
+
+bool known_type(int32_t t) { return t == W4A8_F32 || t == W4A8_F16 || t == W4A8_BF16; }
+bool aligned_to(const void *p, int32_t type) { return ((uintptr_t)p & (type == W4A8_F32 ? 3u : 1u)) == 0; }
+
+w4a8_status check_lora_sizes(int64_t M, int64_t K, int32_t L, int32_t R) {
+    W4A8_REQUIRE(M >= 0 && M < (1ll << 31), W4A8_EINVAL, "M=%lld must be in [0, 2^31)", (long long)M);
+    W4A8_REQUIRE(K > 0 && K % 8 == 0 && K <= kLoraMaxK, W4A8_EINVAL, "K=%lld must be a positive multiple of 8 up to 2^20",
+                 (long long)K);
+    W4A8_REQUIRE(L >= 1 && L <= kLoraMaxL, W4A8_EINVAL, "L=%d must be in [1, 65536]", (int)L);
+    W4A8_REQUIRE(R >= 8 && R % 8 == 0 && R <= kLoraMaxR, W4A8_EINVAL, "R=%d must be a multiple of 8 in [8, 256]", (int)R);
+    return W4A8_OK;
+}
+
+}  // namespace
+
+size_t w4a8_lora_workspace_size(int64_t M, int64_t K, int32_t L, int32_t R) {
+    if (check_lora_sizes(M, K, L, R) != W4A8_OK) return 0;
+    return (size_t)lora_ws_bytes(M, K, L, R);
+}
+
+w4a8_status w4a8_lora_add(const void *x, int32_t x_type, int64_t ldx, int64_t M, int64_t K, const int32_t *row_adapter,
+                          const void *A, const void *B, int32_t ab_type, int32_t L, int32_t R, const int32_t *ranks,
+                          const float *scale, const void *base, int64_t ldb, int64_t N, void *out, int32_t out_type,
+                          int64_t ldo, void *workspace, size_t ws_bytes, hipStream_t stream) {
+    clear_error();
+    if (w4a8_status st = check_lora_sizes(M, K, L, R)) return st;
+    W4A8_REQUIRE(A && B && (M == 0 || (x && row_adapter && base && out && workspace)), W4A8_EINVAL, "null pointer");
+    W4A8_REQUIRE(N >= 1 && N <= kLoraMaxN, W4A8_EINVAL, "N=%lld must be in [1, 2^23]", (long long)N);
+    W4A8_REQUIRE(ldx >= K && ldb >= N && ldo >= N, W4A8_EINVAL, "row strides must be at least K=%lld (x), N=%lld (base, out)",
+                 (long long)K, (long long)N);
+    W4A8_REQUIRE(known_type(x_type), W4A8_EUNSUPPORTED, "x_type=%d is not a supported type", (int)x_type);
+    W4A8_REQUIRE(ab_type == W4A8_F16 || ab_type == W4A8_BF16, W4A8_EUNSUPPORTED,
+                 "ab_type=%d is not a supported type (fp16 or bf16)", (int)ab_type);
+    W4A8_REQUIRE(known_type(out_type), W4A8_EUNSUPPORTED, "out_type=%d is not a supported type", (int)out_type);
+    W4A8_REQUIRE(aligned16(A) && aligned16(B) && aligned16(workspace), W4A8_EINVAL,
+                 "A, B and workspace must be 16-byte aligned");
+    W4A8_REQUIRE(aligned_to(x, x_type) && aligned_to(base, out_type) && aligned_to(out, out_type), W4A8_EINVAL,
+                 "x, base and out must be aligned to their elements");
+    W4A8_REQUIRE((((uintptr_t)row_adapter | (uintptr_t)ranks | (uintptr_t)scale) & 3u) == 0, W4A8_EINVAL,
+                 "row_adapter, ranks and scale must be 4-byte aligned");
+    W4A8_REQUIRE(base != out || M <= 1 || ldb == ldo, W4A8_EINVAL, "base is out itself, but their strides differ");
+    W4A8_REQUIRE((int64_t)std::min<size_t>(ws_bytes, INT64_MAX) >= lora_ws_bytes(M, K, L, R), W4A8_EWORKSPACE,
+                 "workspace of %zu bytes, %lld needed", ws_bytes, (long long)lora_ws_bytes(M, K, L, R));
+    if (M == 0) return W4A8_OK;
+    const LoraArgs a{x, row_adapter, A, B, ranks, scale, base, out, workspace, M, K, N, ldx, ldb, ldo, L, R,
+                     x_type, ab_type, out_type};
+    return hip_status(launch_lora_add(a, stream), "lora_add launch");
+}
+
+w4a8_status w4a8_residual_norm_quantize(const void *res, int32_t res_type, int64_t ldr, const void *y, int32_t y_type,
+                                        int64_t ldy, int64_t M, int64_t H, int32_t post, const float *post_w,
+                                        const float *post_b, const void *gate, int32_t gate_type, int64_t ldg,
+                                        double res_scale, double y_scale, void *res_out, int64_t ldro, int32_t pre,
+                                        const float *pre_w, const float *pre_b, double eps, void *z_out,
+                                        int32_t z_type, int64_t ldz, int8_t *qa, float *a_scale, hipStream_t stream) {
+    clear_error();
+    W4A8_REQUIRE(M >= 0 && M < (1ll << 31), W4A8_EINVAL, "M=%lld must be in [0, 2^31)", (long long)M);
+    W4A8_REQUIRE(H >= 1 && H <= kNormMaxH, W4A8_EINVAL, "H=%lld must be in [1, 32768]", (long long)H);
+    W4A8_REQUIRE(post >= W4A8_NORM_NONE && post <= W4A8_NORM_LAYER && pre >= W4A8_NORM_NONE && pre <= W4A8_NORM_LAYER,
+                 W4A8_EUNSUPPORTED, "post=%d, pre=%d: not supported norms", (int)post, (int)pre);
+    W4A8_REQUIRE(known_type(res_type) && (!y || known_type(y_type)) && (!gate || known_type(gate_type)) &&
+                     (!z_out || known_type(z_type)),
+                 W4A8_EUNSUPPORTED, "a type is not supported");
+    if (M == 0) return W4A8_OK;
+    W4A8_REQUIRE(res || y, W4A8_EINVAL, "null pointer: res or y is needed");
+    W4A8_REQUIRE(y || (post == W4A8_NORM_NONE && !gate), W4A8_EINVAL, "post or gate without y");
+    W4A8_REQUIRE((post != W4A8_NORM_NONE || (!post_w && !post_b)) && (pre != W4A8_NORM_NONE || (!pre_w && !pre_b)),
+                 W4A8_EINVAL, "weights of a norm that is not taken");
+    W4A8_REQUIRE(res_out || z_out || qa, W4A8_EINVAL, "null pointer: an output is needed");
+    W4A8_REQUIRE(!qa == !a_scale, W4A8_EINVAL, "qa and a_scale come together");
+    W4A8_REQUIRE((!res || ldr >= H) && (!y || ldy >= H) && (!gate || ldg == 0 || ldg >= H) && (!res_out || ldro >= H) &&
+                     (!z_out || ldz >= H),
+                 W4A8_EINVAL, "row strides must be at least H=%lld", (long long)H);
+    W4A8_REQUIRE(aligned_to(res, res_type) && aligned_to(y, y_type) && aligned_to(gate, gate_type) &&
+                     aligned_to(res_out, res_type) && aligned_to(z_out, z_type) && aligned16(qa) &&
+                     (((uintptr_t)post_w | (uintptr_t)post_b | (uintptr_t)pre_w | (uintptr_t)pre_b |
+                       (uintptr_t)a_scale) & 3u) == 0,
+                 W4A8_EINVAL, "qa must be 16-byte aligned, the others aligned to their elements");
+    W4A8_REQUIRE(std::isfinite(eps) && eps > 0 && std::isfinite(res_scale) && std::isfinite(y_scale), W4A8_EINVAL,
+                 "eps must be positive, the scales finite");
+    // an output that is an input has its layout, so that every element is read by the thread that writes it
+    const auto same = [&](const void *o, int32_t ot, int64_t lo, const void *i, int32_t it, int64_t li) {
+        return !o || o != i || (ot == it && (M == 1 || lo == li));
+    };
+    W4A8_REQUIRE(!(res_out && res_out == z_out), W4A8_EINVAL, "res_out and z_out are the same memory");
+    W4A8_REQUIRE(same(res_out, res_type, ldro, res, res_type, ldr) && same(res_out, res_type, ldro, y, y_type, ldy) &&
+                     same(res_out, res_type, ldro, gate, gate_type, ldg) && same(z_out, z_type, ldz, res, res_type, ldr) &&
+                     same(z_out, z_type, ldz, y, y_type, ldy) && same(z_out, z_type, ldz, gate, gate_type, ldg),
+                 W4A8_EINVAL, "an output that is an input needs its type and stride");
+    const NormArgs a{res, y, gate, res_out, z_out, post_w, post_b, pre_w, pre_b, qa, a_scale, M, H, ldr, ldy, ldg, ldro,
+                     ldz, res_scale, y_scale, eps, res_type, y_type, gate_type, z_type, post, pre};
+    return hip_status(launch_residual_norm_quantize(a, stream), "residual_norm_quantize launch");
 }
 
 w4a8_status w4a8_moe_route_scored(const void *logits, int32_t logits_type, int64_t ldl, const float *bias, int64_t T,
