@@ -65,7 +65,7 @@ NORM = dict(res=F, rt=0, ldr=64, y=F, yt=0, ldy=64, M=4, H=64, post=1, pw=None, 
     ({"ldr": 63}, EINVAL), ({"ldy": 63}, EINVAL), ({"ldro": 63}, EINVAL), ({"ldz": 63}, EINVAL), ({"gate": F, "ldg": 63}, EINVAL),
     ({"gate": F, "ldg": -1}, EINVAL), ({"res": off(2)}, EINVAL), ({"y": off(1), "yt": 1}, EINVAL), ({"ro": off(2)}, EINVAL),
     ({"z": off(2)}, EINVAL), ({"gate": off(2)}, EINVAL), ({"qa": off(8)}, EINVAL), ({"sc": off(2)}, EINVAL), ({"pw": off(2)}, EINVAL),
-    ({"qw": off(1)}, EINVAL), ({"eps": 0.0}, EINVAL), ({"eps": -1e-6}, EINVAL), ({"eps": float("nan")}, EINVAL),
+    ({"qw": off(1)}, EINVAL), ({"eps": 0.0}, EINVAL), ({"eps": 1e-41}, EINVAL), ({"eps": -1e-6}, EINVAL), ({"eps": float("nan")}, EINVAL),
     ({"rs": float("inf")}, EINVAL), ({"ys": float("nan")}, EINVAL), ({"z": off(65536)}, EINVAL),
     ({"ro": F, "ldro": 65}, EINVAL), ({"ro": F, "rt": 0, "yt": 1}, EINVAL), ({"z": F, "zt": 2}, EINVAL), ({"z": F, "ldz": 72}, EINVAL),
     ({"M": 0, "res": None, "y": None, "ro": None, "z": None, "qa": None, "sc": None, "post": 0}, 0)])

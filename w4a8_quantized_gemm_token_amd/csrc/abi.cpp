@@ -580,8 +580,8 @@ w4a8_status w4a8_residual_norm_quantize(const void *res, int32_t res_type, int64
                      (((uintptr_t)post_w | (uintptr_t)post_b | (uintptr_t)pre_w | (uintptr_t)pre_b |
                        (uintptr_t)a_scale) & 3u) == 0,
                  W4A8_EINVAL, "qa must be 16-byte aligned, the others aligned to their elements");
-    W4A8_REQUIRE(std::isfinite(eps) && eps > 0 && std::isfinite(res_scale) && std::isfinite(y_scale), W4A8_EINVAL,
-                 "eps must be positive, the scales finite");
+    W4A8_REQUIRE(std::isfinite(eps) && eps >= 1e-40 && std::isfinite(res_scale) && std::isfinite(y_scale), W4A8_EINVAL,
+                 "eps must be at least 1e-40, the scales finite");
     // an output that is an input has its layout, so that every element is read by the thread that writes it
     const auto same = [&](const void *o, int32_t ot, int64_t lo, const void *i, int32_t it, int64_t li) {
         return !o || o != i || (ot == it && (M == 1 || lo == li));

@@ -1,8 +1,10 @@
 // norm_kernels.hip -- between two blocks of a model: the post-norm of a block's output, its gate
 // and the residual join, the next block's norm, and the INT8 codes that its products read.
 //
-// The simple form: a workgroup per row that reads the row again for every reduction.  The
-// arithmetic up to z is fp64 (see the entry point).
+// One workgroup per row, the row in registers: y and the stream are read once, everything is
+// written once.  The arithmetic up to z is fp64 (see the entry point).  A row passes up to five
+// reductions (mean and mean square of each norm, the maximum); each is four DPP steps inside 16
+// lanes, four scalar reads, one LDS exchange and one barrier.
 #include "block_internal.hpp"
 
 using namespace w4a8;
@@ -10,95 +12,346 @@ using namespace w4a8dev;
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
+constexpr int kMaxThreads = 1024;
 
-__device__ __forceinline__ float value_at(const void *p, int64_t i, int type) {
-    if (type == W4A8_F32) return ((const float *)p)[i];
-    if (type == W4A8_F16) return (float)((const _Float16 *)p)[i];
-    return (float)((const __bf16 *)p)[i];
-}
+// ------------------------------------------------------------------ elements
+// A thread owns C chunks of 8 elements in a row, chunk c from element (c T + t) 8.  Chunks that lie whole in the row
+// are read and written 16 bytes at a time at any alignment of the rows (the type's own).  TAIL: the row's last chunk
+// does not, and goes element by element; its elements past the row's end are 0.  n: elements of the row from the
+// chunk's first on; chunks with none are skipped.
+// Loads keep the bits of the type, and what uses them converts: a conversion beside the load would wait for it there,
+// before the next load is under way.
+template <typename T>
+using Eight = T __attribute__((ext_vector_type(8)));
 
-// v as its type holds it, through fp32
-__device__ __forceinline__ float rounded(float v, int type) {
-    if (type == W4A8_F16) return (float)(_Float16)v;
-    if (type == W4A8_BF16) return (float)(__bf16)v;
-    return v;
+template <bool TAIL, typename T>
+__device__ __forceinline__ Eight<T> load8(const T *p, int n) {
+    typedef T t8 __attribute__((ext_vector_type(8), aligned(sizeof(T))));
+    if (!TAIL || n >= 8) return *reinterpret_cast<const t8 *>(p);
+    Eight<T> x = {};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < n) x[e] = p[e];
+    return x;
 }
-__device__ __forceinline__ void store_at(void *p, int64_t i, int type, float v) {
-    if (type == W4A8_F32) ((float *)p)[i] = v;
-    else if (type == W4A8_F16) ((_Float16 *)p)[i] = (_Float16)v;
-    else ((__bf16 *)p)[i] = (__bf16)v;
+// The same of a type known at run time: fp32 in both, 16 bits in the first half.
+struct Bits8 {
+    v4u lo, hi;
+};
+template <bool TAIL>
+__device__ __forceinline__ Bits8 load8(const void *p, int64_t at, int type, int n) {
+    Bits8 b;
+    if (type == W4A8_F32) b = __builtin_bit_cast(Bits8, load8<TAIL>((const float *)p + at, n));
+    else b.lo = __builtin_bit_cast(v4u, load8<TAIL>((const _Float16 *)p + at, n));
+    return b;
 }
-
-template <typename T, typename Op>
-__device__ T block_all(T v, T *red, Op op) {
-    for (int o = 32; o > 0; o >>= 1) v = op(v, __shfl_xor(v, o, kWave));
-    __syncthreads();
-    if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = v;
-    __syncthreads();
-    v = red[0];
-    for (int i = 1; i < kWaves; ++i) v = op(v, red[i]);
-    return v;
-}
-
-__global__ __launch_bounds__(kThreads) void norm_kernel(const NormArgs a, int64_t m0) {
-    __shared__ double red[kWaves];
-    __shared__ float fred[kWaves];
-    __shared__ float row[kNormMaxH];  // the stream's row, then z's
-    const int64_t m = m0 + blockIdx.x;
-    const int H = (int)a.H, t = threadIdx.x;
-    const auto add = [](double p, double q) { return p + q; };
-    // mean and 1 / sqrt(mean square + eps) of a row of values
-    const auto stats = [&](int kind, auto at, double &mean, double &inv) {
-        mean = 0.0;
-        inv = 1.0;
-        if (kind == W4A8_NORM_NONE) return;
-        double s = 0.0;
-        if (kind == W4A8_NORM_LAYER) {
-            for (int h = t; h < H; h += kThreads) s += at(h);
-            mean = block_all(s, red, add) / H;
-            s = 0.0;
-        }
-        for (int h = t; h < H; h += kThreads) {
-            const double d = at(h) - mean;
-            s = fma(d, d, s);
-        }
-        inv = 1.0 / sqrt(block_all(s, red, add) / H + a.eps);
+__device__ __forceinline__ void convert(const Bits8 &b, int type, float *v) {
+    const auto from = [&](const auto &x) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = (float)x[e];
     };
-    const auto y_at = [&](int h) { return (double)value_at(a.y, m * a.ldy + h, a.y_type); };
-    double mean = 0.0, inv = 1.0;
-    if (a.y) stats(a.post, y_at, mean, inv);
-    for (int h = t; h < H; h += kThreads) {
-        double v = 0.0;
-        if (a.y) {
-            v = (y_at(h) - mean) * inv;
-            if (a.post_w) v *= a.post_w[h];
-            if (a.post_b) v += a.post_b[h];
-            if (a.gate) v *= value_at(a.gate, m * a.ldg + h, a.gate_type);
-            v *= a.y_scale;
-        }
-        if (a.res) v += a.res_scale * value_at(a.res, m * a.ldr + h, a.res_type);
-        const float r = (float)v;
-        if (a.res_out) store_at(a.res_out, m * a.ldro + h, a.res_type, r);
-        row[h] = rounded(r, a.res_type);
+    if (type == W4A8_F32) from(__builtin_bit_cast(Eight<float>, b));
+    else if (type == W4A8_F16) from(__builtin_bit_cast(Eight<_Float16>, b.lo));
+    else from(__builtin_bit_cast(Eight<__bf16>, b.lo));
+}
+template <bool TAIL, typename T>
+__device__ __forceinline__ void store8(T *p, int n, const float *v) {
+    if (!TAIL || n >= 8) {
+        typedef T t8 __attribute__((ext_vector_type(8), aligned(sizeof(T))));
+        t8 x;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = (T)v[e];
+        *reinterpret_cast<t8 *>(p) = x;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n) p[e] = (T)v[e];
     }
-    stats(a.pre, [&](int h) { return (double)row[h]; }, mean, inv);  // each thread reads what it wrote
+}
+template <bool TAIL>
+__device__ __forceinline__ void store8(void *p, int64_t at, int type, int n, const float *v) {
+    if (type == W4A8_F32) store8<TAIL>((float *)p + at, n, v);
+    else if (type == W4A8_F16) store8<TAIL>((_Float16 *)p + at, n, v);
+    else store8<TAIL>((__bf16 *)p + at, n, v);
+}
+
+// ------------------------------------------------------------------ reductions
+template <int CTRL>
+__device__ __forceinline__ double dpp_add(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (uint32_t)b, CTRL, 0xF, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (uint32_t)(b >> 32), CTRL, 0xF, 0xF, false);
+    return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double lane_of(double v, int lane) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)b, lane), hi = __builtin_amdgcn_readlane((uint32_t)(b >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double row16_sum(double v) {
+    v = dpp_add<0xB1>(v);      // quad_perm [1,0,3,2]
+    v = dpp_add<0x4E>(v);      // quad_perm [2,3,0,1]
+    v = dpp_add<0x124>(v);     // row_ror:4
+    return dpp_add<0x128>(v);  // row_ror:8
+}
+__device__ __forceinline__ double wave_sum(double v) {
+    v = row16_sum(v);
+    return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
+}
+
+// Sums and maxima over the workgroup.  Two exchange buffers in turn: a wave writes one only after
+// the barrier of the reduction between, which every wave passes after it has read it.
+struct Block {
+    double *red;  // [2][16]
+    int waves, turn = 0;
+
+    __device__ __forceinline__ double sum(double v) {
+        v = wave_sum(v);
+        if (waves == 1) return v;
+        double *r = red + 16 * (turn ^= 1);
+        if (threadIdx.x % kWave == 0) r[threadIdx.x / kWave] = v;
+        __syncthreads();
+        const int i = threadIdx.x % 16;
+        return row16_sum(i < waves ? r[i] : 0.0);
+    }
+    // of values that are not negative
+    __device__ __forceinline__ float max(float v) {
+        v = wave_max(v);
+        if (waves == 1) return v;
+        float *r = reinterpret_cast<float *>(red + 16 * (turn ^= 1));
+        if (threadIdx.x % kWave == 0) r[threadIdx.x / kWave] = v;
+        __syncthreads();
+        const int i = threadIdx.x % 16;
+        v = i < waves ? r[i] : 0.0f;
+        v = dpp_max<0xB1>(v);
+        v = dpp_max<0x4E>(v);
+        v = dpp_max<0x124>(v);
+        return dpp_max<0x128>(v);
+    }
+};
+
+// 1 / sqrt(x) and 1 / x in fp64: the hardware's estimate (about 2^-24) and two Newton steps, each of which squares
+// the error, so a few 2^-53 where the library's root and quotient take some sixty instructions in every lane.
+__device__ __forceinline__ double rsqrt64(double x) {
+    double y = __builtin_amdgcn_rsq(x);
+    const double y0 = y;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const double e = fma(-x * y, y, 1.0);
+        y = fma(0.5 * y, e, y);
+    }
+    return x == __builtin_inf() ? y0 : y;  // 0
+}
+__device__ __forceinline__ double rcp64(double x) {
+    double y = __builtin_amdgcn_rcp(x);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) y = fma(fma(-x, y, 1.0), y, y);
+    return y;
+}
+
+// Mean (LAYER) and 1 / sqrt(mean square about it + eps) of the row in v.
+template <typename T, int C, bool TAIL>
+__device__ __forceinline__ void stats(int kind, const Eight<T> (&v)[C], const int (&n)[C], double inv_h, double eps,
+                                      Block &b, double &mean, double &inv) {
+    mean = 0.0;
+    inv = 1.0;
+    if (kind == W4A8_NORM_NONE) return;
+    double s = 0.0;
+    if (kind == W4A8_NORM_LAYER) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            if (n[c] > 0) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s += (double)(float)v[c][e];
+            }
+        mean = b.sum(s) * inv_h;
+        s = 0.0;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            if (n[c] > 0) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const double d = !TAIL || e < n[c] ? (double)(float)v[c][e] - mean : 0.0;
+                    s = fma(d, d, s);
+                }
+            }
+    } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            if (n[c] > 0) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s = fma((double)(float)v[c][e], (double)(float)v[c][e], s);
+            }
+    }
+    inv = rsqrt64(fma(b.sum(s), inv_h, eps));
+}
+
+template <typename TY, typename TR, int C, bool TAIL>
+__global__ __launch_bounds__(kMaxThreads) void norm_kernel(const NormArgs a, double inv_h, int64_t m0) {
+    __shared__ double red[32];
+    const int64_t m = m0 + blockIdx.x;
+    const int H = (int)a.H, t = threadIdx.x, T = blockDim.x;
+    Block b{red, T / kWave};
+    // the row, and one chunk's vectors ahead of the reduction that their use waits for
+    Eight<TY> y[C];
+    Eight<TR> x[C];
+    Eight<float> w;
+    Bits8 g;
+    int n[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int h = (c * T + t) * 8;
+        n[c] = H - h;
+        if (n[c] <= 0) continue;
+        if (a.y) y[c] = load8<TAIL>((const TY *)a.y + m * a.ldy + h, n[c]);
+        if (a.res) x[c] = load8<TAIL>((const TR *)a.res + m * a.ldr + h, n[c]);
+    }
+    if (n[0] > 0) {
+        if (a.post_w) w = load8<TAIL>(a.post_w + t * 8, n[0]);
+        if (a.gate) g = load8<TAIL>(a.gate, m * a.ldg + t * 8, a.gate_type, n[0]);
+    }
+    double mean, inv;
+    if (a.y) stats<TY, C, TAIL>(a.post, y, n, inv_h, a.eps, b, mean, inv);
+    const double first = a.post_b ? inv : inv * a.y_scale;
+    Eight<float> r[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        if (n[c] <= 0) continue;
+        const int h = (c * T + t) * 8;
+        double v[8];
+        if (a.y) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = (double)(float)y[c][e];
+            if (a.post == W4A8_NORM_LAYER) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] -= mean;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= first;
+            if (a.post_w) {
+                if (c) w = load8<TAIL>(a.post_w + h, n[c]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= (double)w[e];
+            }
+            if (a.post_b) {
+                const Eight<float> o = load8<TAIL>(a.post_b + h, n[c]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = (v[e] + (double)o[e]) * a.y_scale;
+            }
+            if (a.gate) {
+                if (c) g = load8<TAIL>(a.gate, m * a.ldg + h, a.gate_type, n[c]);
+                float f[8];
+                convert(g, a.gate_type, f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= (double)f[e];
+            }
+            if (a.res) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = fma((double)(float)x[c][e], a.res_scale, v[e]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = (double)(float)x[c][e] * a.res_scale;
+        }
+        // rounded to fp32 and to the stream's type
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[c][e] = f[e] = !TAIL || e < n[c] ? (float)(TR)(float)v[e] : 0.0f;
+        if (a.res_out) store8<TAIL>((TR *)a.res_out + m * a.ldro + h, n[c], f);
+    }
+    if (a.pre_w && n[0] > 0) w = load8<TAIL>(a.pre_w + t * 8, n[0]);
+    stats<float, C, TAIL>(a.pre, r, n, inv_h, a.eps, b, mean, inv);
     float top = 0.0f;
-    for (int h = t; h < H; h += kThreads) {
-        double v = ((double)row[h] - mean) * inv;
-        if (a.pre_w) v *= a.pre_w[h];
-        if (a.pre_b) v += a.pre_b[h];
-        const float z = (float)v;
-        if (a.z) store_at(a.z, m * a.ldz + h, a.z_type, z);
-        row[h] = z;
-        top = fmaxf(top, fabsf(z));
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        if (n[c] <= 0) continue;
+        const int h = (c * T + t) * 8;
+        double v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = (double)r[c][e];
+        if (a.pre == W4A8_NORM_LAYER) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] -= mean;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= inv;
+        if (a.pre_w) {
+            if (c) w = load8<TAIL>(a.pre_w + h, n[c]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= (double)w[e];
+        }
+        if (a.pre_b) {
+            const Eight<float> o = load8<TAIL>(a.pre_b + h, n[c]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += (double)o[e];
+        }
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            r[c][e] = f[e] = (float)v[e];
+            if (!TAIL || e < n[c]) top = fmaxf(top, fabsf(f[e]));
+        }
+        if (a.z) store8<TAIL>(a.z, m * a.ldz + h, a.z_type, n[c], f);
     }
     if (!a.qa) return;
-    top = block_all(top, fred, [](float p, float q) { return fmaxf(p, q); });
-    const float s = top * (1.0f / 127.0f);
+    const float s = b.max(top) * (1.0f / 127.0f);
     if (t == 0) a.a_scale[m] = s;
-    for (int h = t; h < H; h += kThreads) a.qa[m * H + h] = (int8_t)quantize_i8(row[h], s);
+    // The fp32 quotient z / s, rounded to nearest: z times the fp64 reciprocal of s is within 2^-51 of it, relative,
+    // and a quotient of two 24-bit numbers is 2^-49 away from the middle of two fp32 numbers at least.
+    const double to_code = s == 0.0f ? 0.0 : rcp64((double)s);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        if (n[c] <= 0) continue;
+        const int h = (c * T + t) * 8;
+        int q[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float f = __builtin_rintf((float)((double)r[c][e] * to_code));
+            q[e] = (int)fminf(fmaxf(f, -127.0f), 127.0f);
+        }
+        int8_t *out = a.qa + m * H + h;
+        if (!TAIL || n[c] >= 8) {
+            typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(1)));
+            u2 o;
+            o.x = (q[0] & 0xFF) | (q[1] & 0xFF) << 8 | (q[2] & 0xFF) << 16 | (uint32_t)q[3] << 24;
+            o.y = (q[4] & 0xFF) | (q[5] & 0xFF) << 8 | (q[6] & 0xFF) << 16 | (uint32_t)q[7] << 24;
+            *reinterpret_cast<u2 *>(out) = o;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < n[c]) out[e] = (int8_t)q[e];
+        }
+    }
+}
+
+template <typename TY, typename TR>
+hipError_t launch_typed(const NormArgs &a, hipStream_t stream) {
+    // a thread for each chunk of 8, and more chunks a thread only where 1024 threads do not hold the row
+    const int chunks = (int)((a.H + 7) / 8);
+    const int C = chunks <= kMaxThreads ? 1 : chunks <= 2 * kMaxThreads ? 2 : 4;
+    const int T = ((chunks + C - 1) / C + 63) / 64 * 64;
+    const double inv_h = 1.0 / (double)a.H;
+    const bool tail = a.H % 8 != 0;
+    constexpr int64_t kRows = 1 << 21;  // rows per launch: fewer than 2^32 threads
+    for (int64_t m0 = 0; m0 < a.M; m0 += kRows) {
+        const dim3 grid((uint32_t)(a.M - m0 < kRows ? a.M - m0 : kRows));
+#define W4A8_NORM(CC)                                                                             \
+    (tail ? norm_kernel<TY, TR, CC, true><<<grid, T, 0, stream>>>(a, inv_h, m0)                   \
+          : norm_kernel<TY, TR, CC, false><<<grid, T, 0, stream>>>(a, inv_h, m0))
+        if (C == 1) W4A8_NORM(1);
+        else if (C == 2) W4A8_NORM(2);
+        else W4A8_NORM(4);
+#undef W4A8_NORM
+        if (hipError_t err = hipGetLastError(); err != hipSuccess) return err;
+    }
+    return hipSuccess;
+}
+
+template <typename TY>
+hipError_t launch_y(const NormArgs &a, hipStream_t stream) {
+    if (a.res_type == W4A8_F32) return launch_typed<TY, float>(a, stream);
+    if (a.res_type == W4A8_F16) return launch_typed<TY, _Float16>(a, stream);
+    return launch_typed<TY, __bf16>(a, stream);
 }
 
 }  // namespace
@@ -106,12 +359,9 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(const NormArgs a, int64_
 namespace w4a8 {
 
 hipError_t launch_residual_norm_quantize(const NormArgs &a, hipStream_t stream) {
-    constexpr int64_t kRows = 1 << 22;  // rows per launch: fewer than 2^32 threads
-    for (int64_t m0 = 0; m0 < a.M; m0 += kRows) {
-        norm_kernel<<<dim3((uint32_t)(a.M - m0 < kRows ? a.M - m0 : kRows)), kThreads, 0, stream>>>(a, m0);
-        if (hipError_t err = hipGetLastError(); err != hipSuccess) return err;
-    }
-    return hipSuccess;
+    if (!a.y || a.y_type == W4A8_F32) return launch_y<float>(a, stream);
+    if (a.y_type == W4A8_F16) return launch_y<_Float16>(a, stream);
+    return launch_y<__bf16>(a, stream);
 }
 
 }  // namespace w4a8
