@@ -7,6 +7,8 @@
 // lanes, four scalar reads, one LDS exchange and one barrier.
 #include "block_internal.hpp"
 
+#include <algorithm>
+
 using namespace w4a8;
 using namespace w4a8dev;
 
@@ -15,12 +17,13 @@ namespace {
 constexpr int kMaxThreads = 1024;
 
 // ------------------------------------------------------------------ elements
-// A thread owns C chunks of 8 elements in a row, chunk c from element (c T + t) 8.  Chunks that lie whole in the row
-// are read and written 16 bytes at a time at any alignment of the rows (the type's own).  TAIL: the row's last chunk
-// does not, and goes element by element; its elements past the row's end are 0.  n: elements of the row from the
-// chunk's first on; chunks with none are skipped.
-// Loads keep the bits of the type, and what uses them converts: a conversion beside the load would wait for it there,
-// before the next load is under way.
+// A thread owns C chunks of 8 elements in a row, chunk c from element (c T + t) 8; n is the number of the row's
+// elements from there on, and chunks with none are skipped.  Chunks that lie whole in the row are read and written 16
+// bytes at a time at any alignment of the rows (the type's own).  TAIL: the row's last chunk does not, and goes element
+// by element, with 0 past the row's end (read as the row's last 8 elements and moved down in registers it took longer:
+// 77 rows of 5003 with a gate per row 9.3 us against 8.4).
+// Loads keep the bits of the type, and what uses them converts: beside the load a conversion would wait for it before
+// the next load is under way (4096 rows of 7168 82 us against 62).
 template <typename T>
 using Eight = T __attribute__((ext_vector_type(8)));
 
@@ -34,31 +37,26 @@ __device__ __forceinline__ Eight<T> load8(const T *p, int n) {
         if (e < n) x[e] = p[e];
     return x;
 }
-// The same of a type known at run time: fp32 in both, 16 bits in the first half.
-struct Bits8 {
-    v4u lo, hi;
-};
-template <bool TAIL>
-__device__ __forceinline__ Bits8 load8(const void *p, int64_t at, int type, int n) {
-    Bits8 b;
-    if (type == W4A8_F32) b = __builtin_bit_cast(Bits8, load8<TAIL>((const float *)p + at, n));
-    else b.lo = __builtin_bit_cast(v4u, load8<TAIL>((const _Float16 *)p + at, n));
-    return b;
-}
-__device__ __forceinline__ void convert(const Bits8 &b, int type, float *v) {
-    const auto from = [&](const auto &x) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = (float)x[e];
-    };
-    if (type == W4A8_F32) from(__builtin_bit_cast(Eight<float>, b));
-    else if (type == W4A8_F16) from(__builtin_bit_cast(Eight<_Float16>, b.lo));
-    else from(__builtin_bit_cast(Eight<__bf16>, b.lo));
-}
 template <bool TAIL, typename T>
-__device__ __forceinline__ void store8(T *p, int n, const float *v) {
+__device__ __forceinline__ Eight<float> floats_at(const void *p, int64_t at, int n) {
+    const Eight<T> x = load8<TAIL>((const T *)p + at, n);
+    Eight<float> v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = (float)x[e];
+    return v;
+}
+template <bool TAIL>
+__device__ __forceinline__ Eight<float> floats_at(const void *p, int64_t at, int type, int n) {
+    if (type == W4A8_F32) return floats_at<TAIL, float>(p, at, n);
+    if (type == W4A8_F16) return floats_at<TAIL, _Float16>(p, at, n);
+    return floats_at<TAIL, __bf16>(p, at, n);
+}
+
+template <bool TAIL, typename T>
+__device__ __forceinline__ void store8(T *p, int n, const Eight<float> &v) {
     if (!TAIL || n >= 8) {
         typedef T t8 __attribute__((ext_vector_type(8), aligned(sizeof(T))));
-        t8 x;
+        Eight<T> x;
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = (T)v[e];
         *reinterpret_cast<t8 *>(p) = x;
@@ -69,7 +67,7 @@ __device__ __forceinline__ void store8(T *p, int n, const float *v) {
     }
 }
 template <bool TAIL>
-__device__ __forceinline__ void store8(void *p, int64_t at, int type, int n, const float *v) {
+__device__ __forceinline__ void store8(void *p, int64_t at, int type, int n, const Eight<float> &v) {
     if (type == W4A8_F32) store8<TAIL>((float *)p + at, n, v);
     else if (type == W4A8_F16) store8<TAIL>((_Float16 *)p + at, n, v);
     else store8<TAIL>((__bf16 *)p + at, n, v);
@@ -192,11 +190,8 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(const NormArgs a, dou
     const int64_t m = m0 + blockIdx.x;
     const int H = (int)a.H, t = threadIdx.x, T = blockDim.x;
     Block b{red, T / kWave};
-    // the row, and one chunk's vectors ahead of the reduction that their use waits for
     Eight<TY> y[C];
     Eight<TR> x[C];
-    Eight<float> w;
-    Bits8 g;
     int n[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -205,10 +200,6 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(const NormArgs a, dou
         if (n[c] <= 0) continue;
         if (a.y) y[c] = load8<TAIL>((const TY *)a.y + m * a.ldy + h, n[c]);
         if (a.res) x[c] = load8<TAIL>((const TR *)a.res + m * a.ldr + h, n[c]);
-    }
-    if (n[0] > 0) {
-        if (a.post_w) w = load8<TAIL>(a.post_w + t * 8, n[0]);
-        if (a.gate) g = load8<TAIL>(a.gate, m * a.ldg + t * 8, a.gate_type, n[0]);
     }
     double mean, inv;
     if (a.y) stats<TY, C, TAIL>(a.post, y, n, inv_h, a.eps, b, mean, inv);
@@ -229,21 +220,19 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(const NormArgs a, dou
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] *= first;
             if (a.post_w) {
-                if (c) w = load8<TAIL>(a.post_w + h, n[c]);
+                const Eight<float> w = floats_at<TAIL, float>(a.post_w, h, n[c]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] *= (double)w[e];
             }
             if (a.post_b) {
-                const Eight<float> o = load8<TAIL>(a.post_b + h, n[c]);
+                const Eight<float> o = floats_at<TAIL, float>(a.post_b, h, n[c]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = (v[e] + (double)o[e]) * a.y_scale;
             }
             if (a.gate) {
-                if (c) g = load8<TAIL>(a.gate, m * a.ldg + h, a.gate_type, n[c]);
-                float f[8];
-                convert(g, a.gate_type, f);
+                const Eight<float> g = floats_at<TAIL>(a.gate, m * a.ldg + h, a.gate_type, n[c]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= (double)f[e];
+                for (int e = 0; e < 8; ++e) v[e] *= (double)g[e];
             }
             if (a.res) {
 #pragma unroll
@@ -254,12 +243,10 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(const NormArgs a, dou
             for (int e = 0; e < 8; ++e) v[e] = (double)(float)x[c][e] * a.res_scale;
         }
         // rounded to fp32 and to the stream's type
-        float f[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[c][e] = f[e] = !TAIL || e < n[c] ? (float)(TR)(float)v[e] : 0.0f;
-        if (a.res_out) store8<TAIL>((TR *)a.res_out + m * a.ldro + h, n[c], f);
+        for (int e = 0; e < 8; ++e) r[c][e] = !TAIL || e < n[c] ? (float)(TR)(float)v[e] : 0.0f;
+        if (a.res_out) store8<TAIL>((TR *)a.res_out + m * a.ldro + h, n[c], r[c]);
     }
-    if (a.pre_w && n[0] > 0) w = load8<TAIL>(a.pre_w + t * 8, n[0]);
     stats<float, C, TAIL>(a.pre, r, n, inv_h, a.eps, b, mean, inv);
     float top = 0.0f;
 #pragma unroll
@@ -276,22 +263,21 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(const NormArgs a, dou
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= inv;
         if (a.pre_w) {
-            if (c) w = load8<TAIL>(a.pre_w + h, n[c]);
+            const Eight<float> w = floats_at<TAIL, float>(a.pre_w, h, n[c]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] *= (double)w[e];
         }
         if (a.pre_b) {
-            const Eight<float> o = load8<TAIL>(a.pre_b + h, n[c]);
+            const Eight<float> o = floats_at<TAIL, float>(a.pre_b, h, n[c]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += (double)o[e];
         }
-        float f[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            r[c][e] = f[e] = (float)v[e];
-            if (!TAIL || e < n[c]) top = fmaxf(top, fabsf(f[e]));
+            r[c][e] = (float)v[e];
+            if (!TAIL || e < n[c]) top = fmaxf(top, fabsf(r[c][e]));
         }
-        if (a.z) store8<TAIL>(a.z, m * a.ldz + h, a.z_type, n[c], f);
+        if (a.z) store8<TAIL>(a.z, m * a.ldz + h, a.z_type, n[c], r[c]);
     }
     if (!a.qa) return;
     const float s = b.max(top) * (1.0f / 127.0f);
@@ -302,14 +288,13 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(const NormArgs a, dou
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         if (n[c] <= 0) continue;
-        const int h = (c * T + t) * 8;
         int q[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float f = __builtin_rintf((float)((double)r[c][e] * to_code));
             q[e] = (int)fminf(fmaxf(f, -127.0f), 127.0f);
         }
-        int8_t *out = a.qa + m * H + h;
+        int8_t *out = a.qa + m * H + (c * T + t) * 8;
         if (!TAIL || n[c] >= 8) {
             typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(1)));
             u2 o;
@@ -326,17 +311,20 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(const NormArgs a, dou
 
 template <typename TY, typename TR>
 hipError_t launch_typed(const NormArgs &a, hipStream_t stream) {
-    // a thread for each chunk of 8, and more chunks a thread only where 1024 threads do not hold the row
+    // Chunks a thread.  One, unless 1024 threads do not hold the row, or more than two rows a CU pass and a row would
+    // take more than 512 threads: 20011 rows of 7168 take 318 us with two and 365 with one (fewer waves meet at each
+    // reduction and do its scalar steps), 64 rows of 8192 6.5 us with two and 6.1 with one; 16384 rows of 1024
+    // 41.2 against 39.3.
     const int chunks = (int)((a.H + 7) / 8);
-    const int C = chunks <= kMaxThreads ? 1 : chunks <= 2 * kMaxThreads ? 2 : 4;
+    const int C = chunks > 2 * kMaxThreads ? 4 : chunks > kMaxThreads || (chunks > kMaxThreads / 2 && a.M > 512) ? 2 : 1;
     const int T = ((chunks + C - 1) / C + 63) / 64 * 64;
     const double inv_h = 1.0 / (double)a.H;
     const bool tail = a.H % 8 != 0;
     constexpr int64_t kRows = 1 << 21;  // rows per launch: fewer than 2^32 threads
     for (int64_t m0 = 0; m0 < a.M; m0 += kRows) {
-        const dim3 grid((uint32_t)(a.M - m0 < kRows ? a.M - m0 : kRows));
-#define W4A8_NORM(CC)                                                                             \
-    (tail ? norm_kernel<TY, TR, CC, true><<<grid, T, 0, stream>>>(a, inv_h, m0)                   \
+        const dim3 grid((uint32_t)std::min(a.M - m0, kRows));
+#define W4A8_NORM(CC)                                                                    \
+    (tail ? norm_kernel<TY, TR, CC, true><<<grid, T, 0, stream>>>(a, inv_h, m0)          \
           : norm_kernel<TY, TR, CC, false><<<grid, T, 0, stream>>>(a, inv_h, m0))
         if (C == 1) W4A8_NORM(1);
         else if (C == 2) W4A8_NORM(2);
