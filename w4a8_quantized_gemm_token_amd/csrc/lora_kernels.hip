@@ -98,16 +98,13 @@ struct Operand<_Float16, _Float16, P> {
 };
 
 // ------------------------------------------------------------------ groups of a tile
-// Calls f(adapter, mask of its lanes) for each distinct valid id, those whose turn modulo `of` is `turn`.
-template <typename F>
-__device__ __forceinline__ void for_each_adapter(int id, bool valid, int turn, int of, F &&f) {
-    uint64_t left = __ballot(valid);
-    for (int c = 0; left; c = c + 1 == of ? 0 : c + 1) {
-        const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-        const uint64_t mask = __ballot(valid && id == a);
-        left &= ~mask;
-        if (c == turn) f(a, mask);
-    }
+// A tile's groups: its distinct valid adapters in the order of their first rows.  Each call takes the next one off
+// `left` (the valid lanes that no group has taken yet) and gives the mask of its lanes.
+__device__ __forceinline__ uint64_t next_group(int id, uint64_t &left, int &adapter) {
+    adapter = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+    const uint64_t mask = __ballot(id == adapter) & left;
+    left &= ~mask;
+    return mask;
 }
 
 __device__ __forceinline__ int rank_of(const LoraArgs &a, int id) {
@@ -209,6 +206,9 @@ __device__ __forceinline__ void shrink_group(const LoraArgs &a, int64_t row0, in
     }
 }
 
+// The workspace: each tile's number of groups, and behind them the parts of v [splits][rows][R].
+constexpr int kCounts = kSlab / kTile;
+
 template <typename X, typename W, int P, int RT>
 __global__ __launch_bounds__(kThreads) void lora_shrink_kernel(const LoraArgs a, int64_t m0, int rows, int turns, int per) {
     __shared__ f4 red[kWaves][RT][kWave];
@@ -218,17 +218,26 @@ __global__ __launch_bounds__(kThreads) void lora_shrink_kernel(const LoraArgs a,
     const int id = row < rows ? a.row_adapter[m0 + row] : -1;
     const int windows = (int)((a.K + kWindow - 1) / kWindow);
     const int w0 = split * per, w1 = min(w0 + per, windows);
-    float *part = (float *)a.ws + (int64_t)split * rows * a.R;
+    float *part = (float *)a.ws + kCounts + (int64_t)split * rows * a.R;
     const int64_t slab = (int64_t)blockIdx.x * kTile, row0 = m0 + slab;
-    for_each_adapter(id, (uint32_t)id < (uint32_t)a.L, turn, turns, [&](int ad, uint64_t mask) {
+    uint64_t left = __ballot((uint32_t)id < (uint32_t)a.L);
+    const bool bare = __ballot(row < rows) != left;
+    int groups = 0;
+    for (; left; ++groups) {
+        int ad;
+        const uint64_t mask = next_group(id, left, ad);
+        if (groups % turns != turn) continue;
         const int rank = rank_of(a, ad);
-        if (j0 >= rank) return;
+        if (j0 >= rank) continue;
         gather_rows(mask, list);
         const int cnt = __popcll(mask);
         if (cnt <= 16) shrink_group<X, W, P, 1, RT>(a, row0, slab, ad, rank, j0, cnt, list, w0, w1, part, red);
         else if (cnt <= 32) shrink_group<X, W, P, 2, RT>(a, row0, slab, ad, rank, j0, cnt, list, w0, w1, part, red);
         else shrink_group<X, W, P, 4, RT>(a, row0, slab, ad, rank, j0, cnt, list, w0, w1, part, red);
-    });
+    }
+    // rows without an adapter are a last group where they are copied
+    if (blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0)
+        ((int *)a.ws)[blockIdx.x] = groups + (bare && a.base != a.out ? 1 : 0);
 }
 
 // ------------------------------------------------------------------ expand
@@ -239,17 +248,30 @@ struct Held {
     static constexpr int kParts = kScaled ? 2 : P;
 };
 
-// Columns: a wave's step is NT matrix tiles of 16 columns, dealt so that a lane's four rows of every tile are NT * 4
-// columns in a row (32 bytes of output): tile q, matrix row 4 g + i is column 4 NT g + 4 q + i.
-template <typename T>
-constexpr int tiles_of() {
-    return sizeof(T) == 4 ? 2 : 4;
-}
+constexpr int kExpandBlocks = 3;  // workgroups a CU
+constexpr int kUnit = 128;  // columns that a workgroup's share of a group is counted in
 
+// Columns of a wave's step of NT matrix tiles, dealt so that a lane has 16 bytes of output columns in a row: piece p of the
+// step is the columns VW (4 p + g) .. + VW - 1 of lane group g, with VW = 4 of fp32 (a tile) or 8 of 16 bits (two tiles).
+template <typename T, int NT>
+struct Columns {
+    static constexpr int VW = 16 / sizeof(T), kPieces = NT * 4 / VW, kStep = 16 * NT;
+    static_assert(kUnit % kStep == 0 && NT % 2 == 0, "a step lies in one unit");
+    typedef T V __attribute__((ext_vector_type(16 / sizeof(T))));
+    typedef T VU __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
+    // column of tile q, matrix row r, within a step
+    static __device__ __forceinline__ int of(int q, int r) {
+        return sizeof(T) == 4 ? 16 * q + r : 32 * (q / 2) + 8 * (r / 4) + 4 * (q % 2) + r % 4;
+    }
+};
+
+// Columns [n0, n1) of a group's rows; n0 is a multiple of kUnit, n1 too or N.
 template <typename W, typename T, int P, int KS, int TT>
 __device__ __forceinline__ void expand_group(const LoraArgs &a, int64_t row0, int id, int rank, int cnt, const uint8_t *list,
                                              const Eight<W> *vp, const float *undo, int64_t n0, int64_t n1) {
-    constexpr int NT = tiles_of<T>(), kStep = 16 * NT, kParts = Held<W, P>::kParts;
+    // the fewer rows and ranks, the more columns a step, for loads under way
+    constexpr int NT = TT * KS <= 1 ? 8 : TT * KS <= 2 ? 4 : 2, kParts = Held<W, P>::kParts;
+    using C = Columns<T, NT>;
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, col = lane % 16, g = lane / 16;
     const float scale = a.scale ? a.scale[id] : 1.0f;
     const W *pb = (const W *)a.B + (int64_t)id * a.N * a.R + 8 * g;
@@ -260,63 +282,71 @@ __device__ __forceinline__ void expand_group(const LoraArgs &a, int64_t row0, in
     for (int t = 0; t < TT; ++t) {
         const int i = t * 16 + col;
         const int64_t row = row0 + list[i < cnt ? i : 0];
-        base[t] = (const T *)a.base + row * a.ldb;
-        out[t] = (T *)a.out + row * a.ldo;
+        base[t] = (const T *)a.base + row * a.ldb + C::VW * g;
+        out[t] = (T *)a.out + row * a.ldo + C::VW * g;
         f[t] = Held<W, P>::kScaled ? scale * undo[i < cnt ? i : 0] : scale;
     }
-    for (int64_t n = n0 + wave * kStep; n < n1; n += kWaves * kStep) {
-        const bool whole = n + kStep <= a.N;
-        const int64_t c = n + 4 * NT * g;  // the lane's columns c .. c + 4 NT - 1
-        typedef T tq __attribute__((ext_vector_type(4 * NT), aligned(sizeof(T))));
-        tq have[TT];
+    for (int64_t n = n0 + wave * C::kStep; n < n1; n += kWaves * C::kStep) {
+        const bool whole = n + C::kStep <= a.N;
+        typename C::V have[TT][C::kPieces];
         if (whole) {
 #pragma unroll
             for (int t = 0; t < TT; ++t)
-                if (t * 16 + col < cnt) have[t] = *reinterpret_cast<const tq *>(base[t] + c);
+                if (t * 16 + col < cnt) {
+#pragma unroll
+                    for (int p = 0; p < C::kPieces; ++p)
+                        have[t][p] = *reinterpret_cast<const typename C::VU *>(base[t] + n + 4 * C::VW * p);
+                }
+        }
+        Eight<W> fb[KS][NT];
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+            const int64_t nn = n + C::of(q, col);
+            const W *p = pb + (nn < a.N ? nn : a.N - 1) * a.R;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) fb[ks][q] = ks * 32 + 8 * g < rank ? load8(p + ks * 32) : zero8<W>();
+        }
+        if (rank & 7) {  // ranks past the adapter's own, whatever they hold
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int q = 0; q < NT; ++q)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) fb[ks][q][e] = ks * 32 + 8 * g + e < rank ? fb[ks][q][e] : (W)0.0f;
         }
         f4 acc[TT][NT] = {};
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             if (ks * 32 >= rank) break;
-            Eight<W> fb[NT];
-            const int rest = rank - ks * 32 - 8 * g;  // ranks from this lane's eight on
-#pragma unroll
-            for (int q = 0; q < NT; ++q) {
-                const int64_t nn = n + 4 * NT * (col / 4) + 4 * q + col % 4;
-                fb[q] = rest > 0 ? load8(pb + (nn < a.N ? nn : a.N - 1) * a.R + ks * 32) : zero8<W>();
-            }
-            if (rank & 7) {  // ranks past the adapter's own, whatever they hold
-#pragma unroll
-                for (int q = 0; q < NT; ++q)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) fb[q][e] = e < rest ? fb[q][e] : (W)0.0f;
-            }
 #pragma unroll
             for (int t = 0; t < TT; ++t)
 #pragma unroll
                 for (int p = 0; p < kParts; ++p) {
                     const Eight<W> fv = vp[((p * KS + ks) * kTile + t * 16 + col) * 4 + g];
 #pragma unroll
-                    for (int q = 0; q < NT; ++q) acc[t][q] = mfma(fb[q], fv, acc[t][q]);
+                    for (int q = 0; q < NT; ++q) acc[t][q] = mfma(fb[ks][q], fv, acc[t][q]);
                 }
         }
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
             if (t * 16 + col >= cnt) continue;
             if (whole) {
-                tq o;
 #pragma unroll
-                for (int q = 0; q < NT; ++q)
+                for (int p = 0; p < C::kPieces; ++p) {
+                    typename C::V o;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[4 * q + i] = (T)((float)have[t][4 * q + i] + f[t] * acc[t][q][i]);
-                *reinterpret_cast<tq *>(out[t] + c) = o;
+                    for (int i = 0; i < C::VW; ++i)
+                        o[i] = (T)((float)have[t][p][i] + f[t] * acc[t][(p * C::VW + i) / 4][i % 4]);
+                    *reinterpret_cast<typename C::VU *>(out[t] + n + 4 * C::VW * p) = o;
+                }
             } else {
 #pragma unroll
-                for (int q = 0; q < NT; ++q)
+                for (int p = 0; p < C::kPieces; ++p)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (c + 4 * q + i < a.N)
-                            out[t][c + 4 * q + i] = (T)((float)base[t][c + 4 * q + i] + f[t] * acc[t][q][i]);
+                    for (int i = 0; i < C::VW; ++i) {
+                        const int64_t c = n + 4 * C::VW * p + i;
+                        if (c + C::VW * g < a.N) out[t][c] = (T)((float)base[t][c] + f[t] * acc[t][(p * C::VW + i) / 4][i % 4]);
+                    }
             }
         }
     }
@@ -332,7 +362,7 @@ __device__ __forceinline__ void stage_v(const LoraArgs &a, int64_t slab, int ran
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = 0.0f;
         if (i >= cnt || j >= rank) return;
-        const float *p = (const float *)a.ws + (slab + list[i]) * a.R + j;
+        const float *p = (const float *)a.ws + kCounts + (slab + list[i]) * a.R + j;
 #pragma unroll 4
         for (int s = 0; s < splits; ++s) {
             const Eight<float> x = load8(p + (int64_t)s * rows * a.R);
@@ -391,43 +421,78 @@ __device__ __forceinline__ void stage_v(const LoraArgs &a, int64_t slab, int ran
     __syncthreads();
 }
 
+// Columns [n0, n1) of cnt rows in list, from base to out, 16 bytes a thread.
 template <typename T>
-__device__ __forceinline__ void copy_rows(const LoraArgs &a, int64_t row0, uint64_t mask, int64_t n0, int64_t n1) {
-    for (; mask; mask &= mask - 1) {
-        const int64_t row = row0 + __builtin_ctzll(mask);
-        for (int64_t n = n0 + threadIdx.x; n < n1; n += kThreads)
-            ((T *)a.out)[row * a.ldo + n] = ((const T *)a.base)[row * a.ldb + n];
+__device__ __forceinline__ void copy_rows(const LoraArgs &a, int64_t row0, int cnt, const uint8_t *list, int64_t n0, int64_t n1) {
+    constexpr int VW = 16 / sizeof(T);
+    typedef T VU __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
+    const int pieces = (int)((n1 - n0 + VW - 1) / VW);
+#pragma unroll 4
+    for (int u = threadIdx.x; u < cnt * pieces; u += kThreads) {
+        const int64_t row = row0 + list[u / pieces], n = n0 + (int64_t)(u % pieces) * VW;
+        const T *p = (const T *)a.base + row * a.ldb + n;
+        T *o = (T *)a.out + row * a.ldo + n;
+        if (n + VW <= n1) {
+            *reinterpret_cast<VU *>(o) = *reinterpret_cast<const VU *>(p);
+        } else {
+            for (int i = 0; n + i < n1; ++i) o[i] = p[i];
+        }
     }
 }
 
+// A fixed grid walks the units in equal runs: unit (group, kUnit columns), columns fastest, so that a workgroup stages
+// a group's v once for all its columns, and tiles of few and of many groups cost what their work costs.
 template <typename W, typename T, int P, int KS>
-__global__ __launch_bounds__(kThreads) void lora_expand_kernel(const LoraArgs a, int64_t m0, int rows, int turns, int splits,
-                                                               int chunk) {
+__global__ __launch_bounds__(kThreads, KS > 4 ? 1 : kExpandBlocks) void lora_expand_kernel(const LoraArgs a, int64_t m0, int rows, int splits) {
     __shared__ Eight<W> vp[Held<W, P>::kParts * KS * kTile * 4];
     __shared__ float undo[kTile];
     __shared__ uint32_t top[kTile];
     __shared__ uint8_t list[kTile];
-    const int turn = blockIdx.z;
-    const int row = blockIdx.x * kTile + threadIdx.x % kWave;
-    const int id = row < rows ? a.row_adapter[m0 + row] : -1;
-    const bool valid = (uint32_t)id < (uint32_t)a.L;
-    const int64_t slab = (int64_t)blockIdx.x * kTile, row0 = m0 + slab;
-    const int64_t n0 = (int64_t)blockIdx.y * chunk, n1 = n0 + chunk < a.N ? n0 + chunk : a.N;
-    const bool copies = a.base != a.out;
-    for_each_adapter(id, valid, turn, turns, [&](int ad, uint64_t mask) {
-        const int rank = rank_of(a, ad);
-        if (rank == 0) {
-            if (copies) copy_rows<T>(a, row0, mask, n0, n1);
-            return;
+    const int lane = threadIdx.x % kWave, tiles = (rows + kTile - 1) / kTile;
+    // groups before each lane's tiles; a lane has kCounts / 64 tiles at most
+    const int mine = (tiles + kWave - 1) / kWave;
+    const int *counts = (const int *)a.ws;
+    int upto = 0;
+    for (int i = 0; i < mine; ++i)
+        if (lane * mine + i < tiles) upto += counts[lane * mine + i];
+    for (int o = 1; o < kWave; o <<= 1) {
+        const int v = __shfl_up(upto, o, kWave);
+        if (lane >= o) upto += v;
+    }
+    const int64_t per = (a.N + kUnit - 1) / kUnit, total = per * __builtin_amdgcn_readlane(upto, kWave - 1);
+    const int64_t u1 = total * (blockIdx.x + 1) / gridDim.x;
+    for (int64_t u = total * blockIdx.x / gridDim.x; u < u1;) {
+        const int group = (int)(u / per);
+        const int64_t first = u - group * per, last = first + (u1 - u) < per ? first + (u1 - u) : per;
+        u += last - first;
+        const int64_t n0 = first * kUnit, n1 = last * kUnit < a.N ? last * kUnit : a.N;
+        // the group's tile, and its number there
+        const int l = __builtin_ctzll(__ballot(upto > group));
+        int k = group - (l ? __builtin_amdgcn_readlane(upto, l - 1) : 0), tile = l * mine;
+        while (k >= counts[tile]) k -= counts[tile++];
+        const int row = tile * kTile + lane;
+        const int id = row < rows ? a.row_adapter[m0 + row] : -1;
+        const int64_t slab = (int64_t)tile * kTile, row0 = m0 + slab;
+        uint64_t left = __ballot((uint32_t)id < (uint32_t)a.L), mask = __ballot(row < rows) & ~left;
+        int ad = -1, rank = 0;
+        if (left) {
+            const uint64_t bare = mask;
+            for (; k >= 0 && left; --k) mask = next_group(id, left, ad);
+            if (k < 0) rank = rank_of(a, ad);
+            else mask = bare;
         }
+        if (rank == 0 && a.base == a.out) continue;
         gather_rows(mask, list);
         const int cnt = __popcll(mask);
+        if (rank == 0) {
+            copy_rows<T>(a, row0, cnt, list, n0, n1);
+            continue;
+        }
         stage_v<W, P, KS>(a, slab, rank, cnt, list, rows, splits, vp, undo, top);
         if (cnt <= 16) expand_group<W, T, P, KS, 1>(a, row0, ad, rank, cnt, list, vp, undo, n0, n1);
         else if (cnt <= 32) expand_group<W, T, P, KS, 2>(a, row0, ad, rank, cnt, list, vp, undo, n0, n1);
         else expand_group<W, T, P, KS, 4>(a, row0, ad, rank, cnt, list, vp, undo, n0, n1);
-    });
-    if (copies && turn == 0) copy_rows<T>(a, row0, __ballot(row < rows && !valid), n0, n1);
+    }
 }
 
 // ------------------------------------------------------------------ launches
@@ -437,11 +502,10 @@ struct Plan {
 Plan plan_of(int64_t rows, int64_t K, int32_t L, int32_t R) {
     const int64_t tiles = (rows + kTile - 1) / kTile, windows = (K + kWindow - 1) / kWindow;
     Plan p;
-    p.turns = (int)std::max<int64_t>(1, std::min<int64_t>({kTile, rows, L, 1024 / tiles}));
-    const int64_t blocks = tiles * p.turns * ((R + 63) / 64);
-    const int64_t splits = std::min((512 + blocks - 1) / blocks, (windows + kWaves - 1) / kWaves);
+    const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(1024 / tiles, (windows + kWaves - 1) / kWaves));
     p.per = (int)((windows + splits - 1) / splits);
     p.splits = (int)((windows + p.per - 1) / p.per);
+    p.turns = (int)std::max<int64_t>(1, std::min<int64_t>({kTile, rows, L, 2048 / (tiles * p.splits)}));
     return p;
 }
 
@@ -459,14 +523,10 @@ void shrink(const LoraArgs &a, int64_t m0, int rows, const Plan &p, hipStream_t 
 template <typename W, typename T, int P>
 void expand(const LoraArgs &a, int64_t m0, int rows, const Plan &p, hipStream_t stream) {
     const int64_t tiles = (rows + kTile - 1) / kTile;
-    const int step = kWaves * 16 * tiles_of<T>();
-    const int64_t blocks = tiles * p.turns;
-    int64_t chunk = step;
-    while (chunk < 4 * step && blocks * ((a.N + chunk - 1) / chunk) > 2048) chunk *= 2;
-    while (blocks * ((a.N + chunk - 1) / chunk) > 1 << 22) chunk *= 2;  // fewer than 2^32 threads
-    const dim3 grid((uint32_t)tiles, (uint32_t)((a.N + chunk - 1) / chunk), p.turns);
-#define W4A8_EXPAND(KS) \
-    lora_expand_kernel<W, T, P, KS><<<grid, kThreads, 0, stream>>>(a, m0, rows, p.turns, p.splits, (int)chunk)
+    // no more workgroups than there can be units, or than are resident
+    const int64_t most = tiles * std::min<int64_t>({kTile, rows, (int64_t)a.L + 1}) * ((a.N + kUnit - 1) / kUnit);
+    const uint32_t grid = (uint32_t)std::min<int64_t>(most, 256 * kExpandBlocks);
+#define W4A8_EXPAND(KS) lora_expand_kernel<W, T, P, KS><<<grid, kThreads, 0, stream>>>(a, m0, rows, p.splits)
     if (a.R <= 32) W4A8_EXPAND(1);
     else if (a.R <= 64) W4A8_EXPAND(2);
     else if (a.R <= 128) W4A8_EXPAND(4);
@@ -500,7 +560,7 @@ int64_t lora_ws_bytes(int64_t M, int64_t K, int32_t L, int32_t R) {
     const int64_t first = std::min(M, kSlab), last = M % kSlab;
     int64_t need = plan_of(first, K, L, R).splits * first;
     if (last) need = std::max(need, plan_of(last, K, L, R).splits * last);
-    return need * R * 4;
+    return (need * R + kCounts) * 4;
 }
 
 hipError_t launch_lora_add(const LoraArgs &a, hipStream_t stream) {
