@@ -23,10 +23,10 @@ LORA = dict(x=F, x_type=0, ldx=256, M=4, K=256, ids=F, A=F, B=F, ab=2, L=8, R=16
 @pytest.mark.parametrize("change,status", [
     ({"x": None}, EINVAL), ({"ids": None}, EINVAL), ({"A": None}, EINVAL), ({"B": None}, EINVAL), ({"base": None}, EINVAL),
     ({"out": None}, EINVAL), ({"ws": None}, EINVAL), ({"M": -1}, EINVAL), ({"M": 1 << 31}, EINVAL), ({"K": 0}, EINVAL),
-    ({"K": -8}, EINVAL), ({"K": 252}, EINVAL), ({"K": (1 << 20) + 8, "ldx": BIG}, EINVAL), ({"ldx": 255}, EINVAL),
+    ({"K": -8}, EINVAL), ({"K": 252}, EINVAL), ({"K": (1 << 20) + 8, "ldx": 1 << 21}, EINVAL), ({"ldx": 255}, EINVAL),
     ({"L": 0}, EINVAL), ({"L": 65537}, EINVAL), ({"R": 0}, EINVAL), ({"R": 12}, EINVAL), ({"R": 264}, EINVAL),
-    ({"R": -8}, EINVAL), ({"N": 0}, EINVAL), ({"N": (1 << 23) + 1, "ldb": BIG, "ldo": BIG}, EINVAL), ({"ldb": 39}, EINVAL),
-    ({"ldo": 39}, EINVAL), ({"ldo": 41}, EINVAL), ({"x_type": 3}, EUNSUPPORTED), ({"ab": 0}, EUNSUPPORTED),
+    ({"R": -8}, EINVAL), ({"N": 0}, EINVAL), ({"N": (1 << 23) + 1, "ldb": (1 << 24) - 1, "ldo": (1 << 24) - 1}, EINVAL), ({"ldb": 39}, EINVAL),
+    ({"ldo": 39}, EINVAL), ({"ldo": 41}, EINVAL), ({"ldx": 1 << 24}, EINVAL), ({"ldb": 1 << 24, "ldo": 1 << 24}, EINVAL), ({"x_type": 3}, EUNSUPPORTED), ({"ab": 0}, EUNSUPPORTED),
     ({"ab": 3}, EUNSUPPORTED), ({"out_type": -1}, EUNSUPPORTED), ({"A": off(8)}, EINVAL), ({"B": off(8)}, EINVAL),
     ({"ws": off(8)}, EINVAL), ({"x": off(2)}, EINVAL), ({"x": off(1), "x_type": 1}, EINVAL), ({"base": off(2)}, EINVAL),
     ({"out": off(2)}, EINVAL), ({"out": off(1), "out_type": 2, "base": off(1)}, EINVAL), ({"ids": off(2)}, EINVAL),

@@ -532,6 +532,7 @@ w4a8_status w4a8_lora_add(const void *x, int32_t x_type, int64_t ldx, int64_t M,
     W4A8_REQUIRE(N >= 1 && N <= kLoraMaxN, W4A8_EINVAL, "N=%lld must be in [1, 2^23]", (long long)N);
     W4A8_REQUIRE(ldx >= K && ldb >= N && ldo >= N, W4A8_EINVAL, "row strides must be at least K=%lld (x), N=%lld (base, out)",
                  (long long)K, (long long)N);
+    W4A8_REQUIRE(ldx < kLoraMaxLd && ldb < kLoraMaxLd && ldo < kLoraMaxLd, W4A8_EINVAL, "row strides must be below 2^24");
     W4A8_REQUIRE(known_type(x_type), W4A8_EUNSUPPORTED, "x_type=%d is not a supported type", (int)x_type);
     W4A8_REQUIRE(ab_type == W4A8_F16 || ab_type == W4A8_BF16, W4A8_EUNSUPPORTED,
                  "ab_type=%d is not a supported type (fp16 or bf16)", (int)ab_type);

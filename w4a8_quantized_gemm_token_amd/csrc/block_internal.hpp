@@ -7,7 +7,7 @@
 namespace w4a8 {
 
 // Limits of w4a8_lora_add and w4a8_residual_norm_quantize (checked by the entry points).
-constexpr int64_t kLoraMaxK = 1ll << 20, kLoraMaxN = 1ll << 23, kNormMaxH = 32768;
+constexpr int64_t kLoraMaxK = 1ll << 20, kLoraMaxN = 1ll << 23, kLoraMaxLd = 1ll << 24, kNormMaxH = 32768;
 constexpr int32_t kLoraMaxL = 65536, kLoraMaxR = 256;
 
 struct LoraArgs {

@@ -21,8 +21,8 @@ using namespace w4a8dev;
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
+constexpr int kShrinkThreads = 512, kShrinkWaves = kShrinkThreads / kWave;
+constexpr int kThreads = 256, kWaves = kThreads / kWave;  // of the expand product
 constexpr int kTile = 64;         // rows of a tile, one a lane
 constexpr int kWindow = 64;       // k of a wave's step: 16 a lane group, two matrix instructions
 constexpr int64_t kSlab = 32768;  // rows per pair of launches
@@ -39,6 +39,16 @@ __device__ __forceinline__ Eight<T> load8(const T *p) {
     typedef T t8 __attribute__((ext_vector_type(8), aligned(sizeof(T))));
     return *reinterpret_cast<const t8 *>(p);
 }
+// The same at a byte offset of the lane from an address that is the wave's: 32 bits a lane instead of 64.
+template <typename T>
+__device__ __forceinline__ Eight<T> load8(const T *p, uint32_t bytes) {
+    return load8((const T *)((const char *)p + bytes));
+}
+template <typename V, typename T>
+__device__ __forceinline__ V &at(T *p, uint32_t bytes) {
+    return *(V *)((char *)p + bytes);
+}
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / kWave); }
 template <typename T>
 __device__ __forceinline__ Eight<T> zero8() {
     Eight<T> z = {};
@@ -47,6 +57,19 @@ __device__ __forceinline__ Eight<T> zero8() {
 
 __device__ __forceinline__ f4 mfma(bf8 a, bf8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
 __device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+
+// A barrier for what passes through LDS.  (__syncthreads would also wait for the stores to memory that are under way.)
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// a / b and what is left, for a < 2^22 and b > 0: the fp32 quotient is off by one at most.  (The compiler's own division
+// takes some forty instructions, and these stand before everything else that a workgroup does.)
+__device__ __forceinline__ int quotient(int a, int b, int &rest) {
+    int q = (int)((float)a * __builtin_amdgcn_rcpf((float)b));
+    rest = a - q * b;
+    if (rest < 0) --q, rest += b;
+    if (rest >= b) ++q, rest -= b;
+    return q;
+}
 
 // ------------------------------------------------------------------ operands in parts
 // part[i] = the next 8 bits of v, cut off; an infinity has no rest.
@@ -98,14 +121,52 @@ struct Operand<_Float16, _Float16, P> {
 };
 
 // ------------------------------------------------------------------ groups of a tile
-// A tile's groups: its distinct valid adapters in the order of their first rows.  Each call takes the next one off
-// `left` (the valid lanes that no group has taken yet) and gives the mask of its lanes.
-__device__ __forceinline__ uint64_t next_group(int id, uint64_t &left, int &adapter) {
-    adapter = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-    const uint64_t mask = __ballot(id == adapter) & left;
-    left &= ~mask;
-    return mask;
+// A tile's groups: its distinct valid adapters in the order of their first rows.  A wave finds the k-th one after another
+// (46 ns each), or, from the ninth on, all at once by comparing every pair of ids.
+constexpr int kInTurn = 8;
+
+// The lanes that hold this lane's id; every lane calls it.  ids: 64 words of LDS, the wave's own.
+__device__ __forceinline__ uint64_t lanes_alike(int id, int *ids) {
+    const int lane = threadIdx.x % kWave;
+    ids[lane] = id;
+    __builtin_amdgcn_wave_barrier();
+    uint32_t half[2] = {0, 0};
+#pragma unroll
+    for (int i = kWave - 4; i >= 0; i -= 4) {
+        const v4i o = *reinterpret_cast<const v4i *>(ids + i);
+#pragma unroll
+        for (int e = 3; e >= 0; --e) half[i / 32] = half[i / 32] + half[i / 32] + (o[e] == id ? 1 : 0);
+    }
+    __builtin_amdgcn_wave_barrier();
+    return (uint64_t)half[1] << 32 | half[0];
 }
+
+// A tile's valid lanes, and the first lanes of its groups; by whole waves.
+struct Tile {
+    int id;
+    uint64_t valid, leaders;
+
+    __device__ __forceinline__ Tile(int id, int32_t L, int *ids) : id(id), valid(__ballot((uint32_t)id < (uint32_t)L)) {
+        uint64_t left = valid;
+        leaders = 0;
+        for (int n = 0; left && n < kInTurn; ++n) {
+            const int first = __builtin_ctzll(left);
+            leaders |= 1ull << first;
+            left &= ~__ballot(id == __builtin_amdgcn_readlane(id, first));
+        }
+        if (left) {
+            const int lane = threadIdx.x % kWave;
+            const uint64_t same = lanes_alike(id, ids);
+            leaders = __ballot((valid >> lane & 1) && __builtin_ctzll(same) == lane);
+        }
+    }
+    __device__ __forceinline__ int groups() const { return __popcll(leaders); }
+    // the first lane of group k
+    __device__ __forceinline__ int leader(int k) const {
+        const int lane = threadIdx.x % kWave;
+        return __builtin_ctzll(__ballot((leaders >> lane & 1) && __popcll(leaders & ((1ull << lane) - 1)) == k));
+    }
+};
 
 __device__ __forceinline__ int rank_of(const LoraArgs &a, int id) {
     const int r = a.ranks ? a.ranks[id] : a.R;
@@ -114,10 +175,129 @@ __device__ __forceinline__ int rank_of(const LoraArgs &a, int id) {
 
 // The lanes of mask in a row in list[]; all threads of the workgroup, between barriers.
 __device__ __forceinline__ void gather_rows(uint64_t mask, uint8_t *list) {
-    __syncthreads();
+    lds_barrier();
     if (threadIdx.x < kTile && (mask >> threadIdx.x & 1))
         list[__popcll(mask & ((1ull << threadIdx.x) - 1))] = (uint8_t)threadIdx.x;
-    __syncthreads();
+    lds_barrier();
+}
+
+// The table of all groups, in the order of tiles and first rows, and behind them one entry for each tile that has rows
+// without an adapter, where those are copied.  The workspace: the head, the table, the parts of v [splits][rows][R].
+struct Group {
+    uint64_t mask;  // rows of the tile
+    int32_t adapter, rank, tile;
+    float scale;
+    int32_t pad[2];
+};
+struct Head {
+    int32_t groups, copies, splits, per;  // per: windows of a range of k
+    int32_t pad[12];
+};
+constexpr int kSelf = 8;  // up to this many tiles the shrink product finds the groups for itself, a wave a tile
+
+__host__ __device__ constexpr int tiles_in(int rows) { return (rows + kTile - 1) / kTile; }
+__host__ __device__ constexpr int64_t parts_at(int rows) {
+    return sizeof(Head) + (int64_t)tiles_in(rows) * ((rows < kTile ? rows : kTile) + 1) * sizeof(Group);
+}
+__device__ __forceinline__ Head *head_of(const LoraArgs &a) { return (Head *)a.ws; }
+__device__ __forceinline__ Group *table_of(const LoraArgs &a) { return (Group *)((Head *)a.ws + 1); }
+__device__ __forceinline__ float *parts_of(const LoraArgs &a, int rows) { return (float *)((char *)a.ws + parts_at(rows)); }
+
+// A tile's entries, its groups from number `at` on and its rows without an adapter at `bare`; every lane calls it.
+__device__ __forceinline__ void write_groups(const LoraArgs &a, const Tile &t, uint64_t in, int tile, int at, int bare) {
+    const int lane = threadIdx.x % kWave;
+    uint64_t mask = 0, left = t.leaders;
+    for (; left; left &= left - 1) {
+        const int first = __builtin_ctzll(left);
+        const uint64_t m = __ballot(t.id == __builtin_amdgcn_readlane(t.id, first)) & t.valid;
+        mask = lane == first ? m : mask;
+    }
+    if (t.leaders >> lane & 1)
+        table_of(a)[at + __popcll(t.leaders & ((1ull << lane) - 1))] =
+            Group{mask, t.id, rank_of(a, t.id), tile, a.scale ? a.scale[t.id] : 1.0f, {0, 0}};
+    if (a.base != a.out && in != t.valid && lane == 0) table_of(a)[bare] = Group{in & ~t.valid, -1, 0, tile, 0.0f, {0, 0}};
+}
+
+// Ranges of k, and windows of each: as many as make kTarget units of all groups and blocks of ranks, or four where there
+// are more units than that already (so that the last round of workgroups is a short one), but no more parts of v than
+// each group's columns are worth reading (kStaged bytes a group on average), and no more than the workspace has room for.
+constexpr int kTarget = 512, kStaged = 65536;
+constexpr int blocks_of(int R) { return R <= 64 ? 1 : (R + 63) / 64; }  // of ranks in the shrink product
+__device__ __forceinline__ void set_ranges(Head &h, int rows, int64_t K, int R, int most) {
+    const int windows = (int)((K + kWindow - 1) / kWindow);
+    const float units = (float)max(1, h.groups * blocks_of(R));
+    const int worth = max(2, (int)(kStaged / 4 * (float)h.groups * __builtin_amdgcn_rcpf((float)(rows * R))));
+    const int wanted = max(1, min(min(max(4, (int)(kTarget * __builtin_amdgcn_rcpf(units))), worth), most));
+    int rest;
+    h.per = quotient(windows + wanted - 1, wanted, rest);
+    h.splits = quotient(windows + h.per - 1, h.per, rest);
+}
+
+// Sums of v over the lanes up to each.
+__device__ __forceinline__ int sum_upto(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+    return v + __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+}
+
+// More tiles: the table by one workgroup, wave w the tiles w, w + 16, ...
+constexpr int kTableThreads = 1024, kTableWaves = kTableThreads / kWave, kMaxTiles = kSlab / kTile;
+__global__ __launch_bounds__(kTableThreads) void lora_table_kernel(const LoraArgs a, int64_t m0, int rows, int most) {
+    __shared__ __attribute__((aligned(16))) int ids[kTableWaves][kWave];
+    __shared__ int counts[kMaxTiles], bare[kMaxTiles];
+    const int lane = threadIdx.x % kWave, wave = wave_id(), tiles = tiles_in(rows);
+    for (int pass = 0; pass < 2; ++pass) {
+        for (int t0 = wave; t0 < tiles; t0 += 4 * kTableWaves) {
+            int id[4];  // under way together
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = (t0 + i * kTableWaves) * kTile + lane;
+                id[i] = row < rows ? a.row_adapter[m0 + row] : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int tile = t0 + i * kTableWaves;
+                if (tile >= tiles) break;
+                const Tile t(id[i], a.L, ids[wave]);
+                const uint64_t in = __ballot(tile * kTile + lane < rows);
+                if (pass) {
+                    write_groups(a, t, in, tile, counts[tile], bare[tile]);
+                } else if (lane == 0) {
+                    counts[tile] = t.groups();
+                    bare[tile] = a.base != a.out && in != t.valid ? 1 : 0;
+                }
+            }
+        }
+        lds_barrier();
+        if (pass == 0) {
+            if (wave == 0) {
+                // counts become the numbers of first groups
+                constexpr int kMine = kMaxTiles / kWave;
+                int c = 0, b = 0;
+                for (int i = 0; i < kMine; ++i)
+                    if (lane * kMine + i < tiles) c += counts[lane * kMine + i], b += bare[lane * kMine + i];
+                const int cs = sum_upto(c), bs = sum_upto(b), groups = __builtin_amdgcn_readlane(cs, kWave - 1);
+                int at = cs - c, bat = groups + bs - b;
+                for (int i = 0; i < kMine; ++i)
+                    if (lane * kMine + i < tiles) {
+                        const int n = counts[lane * kMine + i], f = bare[lane * kMine + i];
+                        counts[lane * kMine + i] = at;
+                        bare[lane * kMine + i] = bat;
+                        at += n;
+                        bat += f;
+                    }
+                if (lane == kWave - 1) {
+                    Head h{groups, bs, 0, 0, {}};
+                    set_ranges(h, rows, a.K, a.R, most);
+                    *head_of(a) = h;
+                }
+            }
+            lds_barrier();
+        }
+    }
 }
 
 // ------------------------------------------------------------------ shrink
@@ -128,18 +308,19 @@ __device__ __forceinline__ void shrink_group(const LoraArgs &a, int64_t row0, in
                                              const uint8_t *list, int w0, int w1, float *part, f4 (*red)[RT][kWave]) {
     using OX = Operand<X, W, P>;
     using OW = Operand<W, X, P>;
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, col = lane % 16, g = lane / 16;
-    const X *px[TT];
+    const int wave = wave_id(), lane = threadIdx.x % kWave, col = lane % 16, g = lane / 16;
+    const X *px = (const X *)a.x + row0 * a.ldx;
+    const W *pw = (const W *)a.A + (int64_t)id * a.R * a.K;
+    uint32_t ox[TT], ow[RT];  // bytes: 64 rows of strides below 2^24, 256 ranks of K up to 2^20
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
         const int i = t * 16 + col;
-        px[t] = (const X *)a.x + (row0 + list[i < cnt ? i : 0]) * a.ldx + 16 * g;
+        ox[t] = (list[i < cnt ? i : 0] * (uint32_t)a.ldx + 16 * g) * (uint32_t)sizeof(X);
     }
-    const W *pw[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
         const int j = j0 + r * 16 + col;
-        pw[r] = (const W *)a.A + ((int64_t)id * a.R + (j < rank ? j : rank - 1)) * a.K + 16 * g;
+        ow[r] = ((uint32_t)(j < rank ? j : rank - 1) * (uint32_t)a.K + 16 * g) * (uint32_t)sizeof(W);
     }
     f4 acc[TT][RT] = {};
     const auto step = [&](const Eight<W> (&rw)[RT][2], const Eight<X> (&rx)[TT][2]) {
@@ -164,7 +345,7 @@ __device__ __forceinline__ void shrink_group(const LoraArgs &a, int64_t row0, in
         }
     };
     const int whole = (int)(a.K / kWindow);
-    for (int w = w0 + wave; w < w1; w += kWaves) {
+    for (int w = w0 + wave; w < w1; w += kShrinkWaves) {
         Eight<W> rw[RT][2];
         Eight<X> rx[TT][2];
         const int64_t k = (int64_t)w * kWindow;
@@ -172,18 +353,18 @@ __device__ __forceinline__ void shrink_group(const LoraArgs &a, int64_t row0, in
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                for (int r = 0; r < RT; ++r) rw[r][h] = load8(pw[r] + k + 8 * h);
+                for (int r = 0; r < RT; ++r) rw[r][h] = load8(pw + k + 8 * h, ow[r]);
 #pragma unroll
-                for (int t = 0; t < TT; ++t) rx[t][h] = load8(px[t] + k + 8 * h);
+                for (int t = 0; t < TT; ++t) rx[t][h] = load8(px + k + 8 * h, ox[t]);
             }
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const bool in = k + 16 * g + 8 * h < a.K;
 #pragma unroll
-                for (int r = 0; r < RT; ++r) rw[r][h] = in ? load8(pw[r] + k + 8 * h) : zero8<W>();
+                for (int r = 0; r < RT; ++r) rw[r][h] = in ? load8(pw + k + 8 * h, ow[r]) : zero8<W>();
 #pragma unroll
-                for (int t = 0; t < TT; ++t) rx[t][h] = in ? load8(px[t] + k + 8 * h) : zero8<X>();
+                for (int t = 0; t < TT; ++t) rx[t][h] = in ? load8(px + k + 8 * h, ox[t]) : zero8<X>();
             }
         }
         step(rw, rx);
@@ -191,53 +372,98 @@ __device__ __forceinline__ void shrink_group(const LoraArgs &a, int64_t row0, in
     // the waves' sums together, and to the workspace: lane has ranks 4 g .. 4 g + 3 of its tile, token col
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
-        if (t) __syncthreads();
+        if (t) lds_barrier();
 #pragma unroll
         for (int r = 0; r < RT; ++r) red[wave][r][lane] = acc[t][r];
-        __syncthreads();
+        lds_barrier();
         const int i = t * 16 + col;
-        for (int r = wave; r < RT; r += kWaves) {
+        for (int r = wave; r < RT; r += kShrinkWaves) {
             const int j = j0 + r * 16 + 4 * g;
             f4 s = red[0][r][lane];
 #pragma unroll
-            for (int w = 1; w < kWaves; ++w) s += red[w][r][lane];
+            for (int w = 1; w < kShrinkWaves; ++w) s += red[w][r][lane];
             if (i < cnt && j < a.R) *reinterpret_cast<f4 *>(part + (slab + list[i]) * a.R + j) = s;
         }
     }
 }
 
-// The workspace: each tile's number of groups, and behind them the parts of v [splits][rows][R].
-constexpr int kCounts = kSlab / kTile;
-
-template <typename X, typename W, int P, int RT>
-__global__ __launch_bounds__(kThreads) void lora_shrink_kernel(const LoraArgs a, int64_t m0, int rows, int turns, int per) {
-    __shared__ f4 red[kWaves][RT][kWave];
+// A fixed grid walks units (group, block of ranks, range of k).  SELF: every workgroup finds the groups, and the first one
+// writes the table for the expand product.
+template <typename X, typename W, int P, int RT, bool SELF>
+__global__ __launch_bounds__(kShrinkThreads) void lora_shrink_kernel(const LoraArgs a, int64_t m0, int rows, int most) {
+    __shared__ f4 red[kShrinkWaves][RT][kWave];
+    __shared__ __attribute__((aligned(16))) int ids[kShrinkWaves][kWave];
+    __shared__ uint64_t masks[kSelf];
+    __shared__ int counts[2][kSelf];
     __shared__ uint8_t list[kTile];
-    const int split = blockIdx.y / turns, turn = blockIdx.y % turns, j0 = blockIdx.z * RT * 16;
-    const int row = blockIdx.x * kTile + threadIdx.x % kWave;
-    const int id = row < rows ? a.row_adapter[m0 + row] : -1;
-    const int windows = (int)((a.K + kWindow - 1) / kWindow);
-    const int w0 = split * per, w1 = min(w0 + per, windows);
-    float *part = (float *)a.ws + kCounts + (int64_t)split * rows * a.R;
-    const int64_t slab = (int64_t)blockIdx.x * kTile, row0 = m0 + slab;
-    uint64_t left = __ballot((uint32_t)id < (uint32_t)a.L);
-    const bool bare = __ballot(row < rows) != left;
-    int groups = 0;
-    for (; left; ++groups) {
-        int ad;
-        const uint64_t mask = next_group(id, left, ad);
-        if (groups % turns != turn) continue;
-        const int rank = rank_of(a, ad);
-        if (j0 >= rank) continue;
-        gather_rows(mask, list);
-        const int cnt = __popcll(mask);
-        if (cnt <= 16) shrink_group<X, W, P, 1, RT>(a, row0, slab, ad, rank, j0, cnt, list, w0, w1, part, red);
-        else if (cnt <= 32) shrink_group<X, W, P, 2, RT>(a, row0, slab, ad, rank, j0, cnt, list, w0, w1, part, red);
-        else shrink_group<X, W, P, 4, RT>(a, row0, slab, ad, rank, j0, cnt, list, w0, w1, part, red);
+    const int lane = threadIdx.x % kWave, wave = wave_id(), tiles = tiles_in(rows);
+    const int windows = (int)((a.K + kWindow - 1) / kWindow), blocks = blocks_of(a.R);
+    Head h;
+    int id = -1;
+    if (SELF) {
+        const int row = wave * kTile + lane;
+        id = row < rows ? a.row_adapter[m0 + row] : -1;
+        const Tile t(id, a.L, ids[wave]);
+        const uint64_t in = __ballot(row < rows);
+        if (lane == 0) {
+            counts[0][wave] = t.groups();
+            counts[1][wave] = a.base != a.out && in != t.valid ? 1 : 0;
+        }
+        ids[wave][lane] = id;
+        if (lane == 0) masks[wave] = t.leaders;
+        lds_barrier();
+        const int c = lane < kSelf ? counts[0][lane] : 0, b = lane < kSelf ? counts[1][lane] : 0;
+        const int cs = sum_upto(c), bs = sum_upto(b);
+        h.groups = __builtin_amdgcn_readlane(cs, kWave - 1);
+        h.copies = __builtin_amdgcn_readlane(bs, kWave - 1);
+        set_ranges(h, rows, a.K, a.R, most);
+        if (blockIdx.x == 0) {
+            if (threadIdx.x == 0) {
+                head_of(a)->groups = h.groups;
+                head_of(a)->copies = h.copies;
+                head_of(a)->splits = h.splits;
+            }
+            if (wave < tiles)
+                write_groups(a, t, in, wave, __builtin_amdgcn_readlane(cs - c, wave),
+                             h.groups + __builtin_amdgcn_readlane(bs - b, wave));
+        }
+        id = cs;  // groups up to and with tile `lane`, for the search below
+    } else {
+        h.groups = head_of(a)->groups;
+        h.splits = head_of(a)->splits;
+        h.per = head_of(a)->per;
     }
-    // rows without an adapter are a last group where they are copied
-    if (blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0)
-        ((int *)a.ws)[blockIdx.x] = groups + (bare && a.base != a.out ? 1 : 0);
+    for (int u = blockIdx.x; u < h.groups * blocks * h.splits; u += gridDim.x) {
+        int split, block;
+        int k = quotient(quotient(u, h.splits, split), blocks, block);
+        const int j0 = block * 16 * RT;
+        Group g;
+        if (SELF) {
+            g.tile = __builtin_ctzll(__ballot(id > k));
+            if (g.tile) k -= __builtin_amdgcn_readlane(id, g.tile - 1);
+            const uint64_t leaders = masks[g.tile];
+            const int mine = ids[g.tile][lane];
+            const int first =
+                __builtin_ctzll(__ballot((leaders >> lane & 1) && __popcll(leaders & ((1ull << lane) - 1)) == k));
+            g.adapter = __builtin_amdgcn_readlane(mine, first);
+            g.mask = __ballot(mine == g.adapter);
+            g.rank = rank_of(a, g.adapter);
+        } else {
+            g = table_of(a)[k];
+            g.tile = __builtin_amdgcn_readfirstlane(g.tile);
+            g.adapter = __builtin_amdgcn_readfirstlane(g.adapter);
+            g.rank = __builtin_amdgcn_readfirstlane(g.rank);
+        }
+        if (j0 >= g.rank) continue;
+        gather_rows(g.mask, list);
+        const int cnt = __builtin_amdgcn_readfirstlane(__popcll(g.mask));
+        const int64_t slab = (int64_t)g.tile * kTile, row0 = m0 + slab;
+        const int w0 = split * h.per, w1 = min(w0 + h.per, windows);
+        float *part = parts_of(a, rows) + (int64_t)split * rows * a.R;
+        if (cnt <= 16) shrink_group<X, W, P, 1, RT>(a, row0, slab, g.adapter, g.rank, j0, cnt, list, w0, w1, part, red);
+        else if (cnt <= 32) shrink_group<X, W, P, 2, RT>(a, row0, slab, g.adapter, g.rank, j0, cnt, list, w0, w1, part, red);
+        else shrink_group<X, W, P, 4, RT>(a, row0, slab, g.adapter, g.rank, j0, cnt, list, w0, w1, part, red);
+    }
 }
 
 // ------------------------------------------------------------------ expand
@@ -247,6 +473,13 @@ struct Held {
     static constexpr bool kScaled = std::is_same<W, _Float16>::value;
     static constexpr int kParts = kScaled ? 2 : P;
 };
+
+// Entries from the n-th on become 0: ranks past the adapter's own, whatever they hold.
+template <typename W>
+__device__ __forceinline__ void cut(Eight<W> &x, int n) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = e < n ? x[e] : (W)0.0f;
+}
 
 constexpr int kExpandBlocks = 3;  // workgroups a CU
 constexpr int kUnit = 128;  // columns that a workgroup's share of a group is counted in
@@ -265,54 +498,60 @@ struct Columns {
     }
 };
 
-// Columns [n0, n1) of a group's rows; n0 is a multiple of kUnit, n1 too or N.
-template <typename W, typename T, int P, int KS, int TT>
-__device__ __forceinline__ void expand_group(const LoraArgs &a, int64_t row0, int id, int rank, int cnt, const uint8_t *list,
-                                             const Eight<W> *vp, const float *undo, int64_t n0, int64_t n1) {
+// Columns [n0, n1) of a group's rows; n0 is a multiple of kUnit, n1 too or N.  stage() puts the group's v into vp and undo.
+template <typename W, typename T, int P, int KS, int TT, typename Stage>
+__device__ __forceinline__ void expand_group(const LoraArgs &a, int64_t row0, int id, int rank, float scale, int cnt, const uint8_t *list,
+                                             const Eight<W> *vp, const float *undo, int64_t n0, int64_t n1, Stage &&stage) {
     // the fewer rows and ranks, the more columns a step, for loads under way
-    constexpr int NT = TT * KS <= 1 ? 8 : TT * KS <= 2 ? 4 : 2, kParts = Held<W, P>::kParts;
+    constexpr int NT = TT * KS <= 2 ? 4 : 2, kParts = Held<W, P>::kParts;
     using C = Columns<T, NT>;
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, col = lane % 16, g = lane / 16;
-    const float scale = a.scale ? a.scale[id] : 1.0f;
-    const W *pb = (const W *)a.B + (int64_t)id * a.N * a.R + 8 * g;
-    const T *base[TT];
-    T *out[TT];
+    const int wave = wave_id(), lane = threadIdx.x % kWave, col = lane % 16, g = lane / 16;
+    const W *pb = (const W *)a.B + (int64_t)id * a.N * a.R;
+    const T *base = (const T *)a.base + row0 * a.ldb;
+    T *out = (T *)a.out + row0 * a.ldo;
+    uint32_t ob[TT], oo[TT], ow[NT];  // bytes: 64 rows of strides below 2^24, 128 columns of 256 ranks
     float f[TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
         const int i = t * 16 + col;
-        const int64_t row = row0 + list[i < cnt ? i : 0];
-        base[t] = (const T *)a.base + row * a.ldb + C::VW * g;
-        out[t] = (T *)a.out + row * a.ldo + C::VW * g;
+        const uint32_t row = list[i < cnt ? i : 0];
+        ob[t] = (row * (uint32_t)a.ldb + C::VW * g) * (uint32_t)sizeof(T);
+        oo[t] = (row * (uint32_t)a.ldo + C::VW * g) * (uint32_t)sizeof(T);
+    }
+#pragma unroll
+    for (int q = 0; q < NT; ++q) ow[q] = (C::of(q, col) * a.R + 8 * g) * (uint32_t)sizeof(W);
+    typename C::V have[TT][C::kPieces];
+    Eight<W> fb[KS][NT];
+    const auto load = [&](int64_t n) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+            if (t * 16 + col < cnt) {
+#pragma unroll
+                for (int p = 0; p < C::kPieces; ++p) have[t][p] = at<const typename C::VU>(base + n + 4 * C::VW * p, ob[t]);
+            }
+#pragma unroll
+        for (int q = 0; q < NT; ++q)
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+                fb[ks][q] = ks * 32 + 8 * g < rank ? load8(pb + n * a.R + ks * 32, ow[q]) : zero8<W>();
+    };
+    const int64_t whole = n0 + (n1 - n0) / C::kStep * C::kStep;  // n1 but for the columns at N's end
+    int64_t n = n0 + wave * C::kStep;
+    // the first step's loads are under way while v is staged, where the registers last
+    if (TT < 4 && n < whole) load(n);
+    stage();
+    if (TT == 4 && n < whole) load(n);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+        const int i = t * 16 + col;
         f[t] = Held<W, P>::kScaled ? scale * undo[i < cnt ? i : 0] : scale;
     }
-    for (int64_t n = n0 + wave * C::kStep; n < n1; n += kWaves * C::kStep) {
-        const bool whole = n + C::kStep <= a.N;
-        typename C::V have[TT][C::kPieces];
-        if (whole) {
-#pragma unroll
-            for (int t = 0; t < TT; ++t)
-                if (t * 16 + col < cnt) {
-#pragma unroll
-                    for (int p = 0; p < C::kPieces; ++p)
-                        have[t][p] = *reinterpret_cast<const typename C::VU *>(base[t] + n + 4 * C::VW * p);
-                }
-        }
-        Eight<W> fb[KS][NT];
-#pragma unroll
-        for (int q = 0; q < NT; ++q) {
-            const int64_t nn = n + C::of(q, col);
-            const W *p = pb + (nn < a.N ? nn : a.N - 1) * a.R;
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) fb[ks][q] = ks * 32 + 8 * g < rank ? load8(p + ks * 32) : zero8<W>();
-        }
-        if (rank & 7) {  // ranks past the adapter's own, whatever they hold
+    for (; n < whole; n += kWaves * C::kStep) {
+        if (rank & 7) {
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                for (int q = 0; q < NT; ++q)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) fb[ks][q][e] = ks * 32 + 8 * g + e < rank ? fb[ks][q][e] : (W)0.0f;
+                for (int q = 0; q < NT; ++q) cut(fb[ks][q], rank - ks * 32 - 8 * g);
         }
         f4 acc[TT][NT] = {};
 #pragma unroll
@@ -328,71 +567,115 @@ __device__ __forceinline__ void expand_group(const LoraArgs &a, int64_t row0, in
                 }
         }
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            if (t * 16 + col >= cnt) continue;
-            if (whole) {
+        for (int t = 0; t < TT; ++t)
+            if (t * 16 + col < cnt) {
 #pragma unroll
                 for (int p = 0; p < C::kPieces; ++p) {
                     typename C::V o;
 #pragma unroll
                     for (int i = 0; i < C::VW; ++i)
                         o[i] = (T)((float)have[t][p][i] + f[t] * acc[t][(p * C::VW + i) / 4][i % 4]);
-                    *reinterpret_cast<typename C::VU *>(out[t] + n + 4 * C::VW * p) = o;
+                    at<typename C::VU>(out + n + 4 * C::VW * p, oo[t]) = o;
                 }
-            } else {
-#pragma unroll
-                for (int p = 0; p < C::kPieces; ++p)
-#pragma unroll
-                    for (int i = 0; i < C::VW; ++i) {
-                        const int64_t c = n + 4 * C::VW * p + i;
-                        if (c + C::VW * g < a.N) out[t][c] = (T)((float)base[t][c] + f[t] * acc[t][(p * C::VW + i) / 4][i % 4]);
-                    }
             }
+        if (n + kWaves * C::kStep < whole) load(n + kWaves * C::kStep);
+    }
+    // the columns at N's end: 16 at a time, element by element, 16 rows a wave
+    for (int u = wave; whole + u / TT * 16 < n1; u += kWaves) {
+        const int i = u % TT * 16 + col;
+        const int64_t c = whole + u / TT * 16, nn = c + col < n1 ? c + col : n1 - 1;
+        f4 acc = {};
+        for (int ks = 0; ks * 32 < rank; ++ks) {
+            Eight<W> b = ks * 32 + 8 * g < rank ? load8(pb + nn * a.R + 8 * g + ks * 32) : zero8<W>();
+            cut(b, rank - ks * 32 - 8 * g);
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) acc = mfma(b, vp[((p * KS + ks) * kTile + i) * 4 + g], acc);
         }
+        if (i >= cnt) continue;
+        const int64_t row = list[i];
+        const float fi = Held<W, P>::kScaled ? scale * undo[i] : scale;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + 4 * g + e < n1) {
+                const float have = (float)base[row * a.ldb + c + 4 * g + e];
+                out[row * a.ldo + c + 4 * g + e] = (T)(have + fi * acc[e]);
+            }
     }
 }
 
-// The rows of v of a group in LDS, as the matrix instruction's columns: vp[part][ks][token][g], 8 ranks each.
+// The rows of v of a group in LDS, as the matrix instruction's columns: vp[part][ks][token][g], 8 ranks each.  Where the
+// group has fewer eights of ranks than there are threads, the ranges of k are shared out over threads too and meet in
+// `some`, so that few rows wait for one or two loads and not for one after another.
 template <typename W, int P, int KS>
 __device__ __forceinline__ void stage_v(const LoraArgs &a, int64_t slab, int rank, int cnt, const uint8_t *list, int rows,
-                                        int splits, Eight<W> *vp, float *undo, uint32_t *top) {
+                                        int splits, Eight<W> *vp, float *undo, uint32_t *top, Eight<float> *some) {
     constexpr int kParts = Held<W, P>::kParts;
-    const int t = threadIdx.x, eights = KS * 4, tokens = (cnt + 15) / 16 * 16;
-    const auto sum = [&](int i, int j, float (&v)[8]) {  // ranks j .. j + 7 of token i
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-        if (i >= cnt || j >= rank) return;
-        const float *p = (const float *)a.ws + kCounts + (slab + list[i]) * a.R + j;
-#pragma unroll 4
-        for (int s = 0; s < splits; ++s) {
-            const Eight<float> x = load8(p + (int64_t)s * rows * a.R);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += x[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = j + e < rank ? v[e] : 0.0f;
-    };
+    const int t = threadIdx.x, tokens = (cnt + 15) / 16 * 16, eights = (rank + 7) / 8;
+    constexpr int all = KS * 4;  // eights of a token, those past the rank 0
+    const float *parts = parts_of(a, rows) + slab * a.R;
+    const int64_t range = (int64_t)rows * a.R;
     if constexpr (Held<W, P>::kScaled) {
-        // the largest finite entry of each row goes to [2^14, 2^15): two fp16 parts then hold 22 bits of it, and
-        // of smaller entries all that lies above 2^-38 of it
         if (t < kTile) top[t] = 0;
-        __syncthreads();
-        for (int u = t; u < tokens * eights; u += kThreads) {
-            const int i = u / eights, j = u % eights * 8;
-            float v[8];
-            sum(i, j, v);
+        lds_barrier();
+    }
+    // entry u of tokens * all: the token, and its eight of ranks
+    const auto put = [&](int u, const Eight<float> &sum) {
+        const int i = u / all, j = u % all;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = i < cnt && j * 8 + e < rank ? sum[e] : 0.0f;
+        if constexpr (Held<W, P>::kScaled) {
             float m = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) m = __builtin_isfinite(v[e]) ? fmaxf(m, fabsf(v[e])) : m;
             if (m > 0.0f) atomicMax(&top[i], __builtin_bit_cast(uint32_t, m));
             // fp32 in the place of the parts until the row's scale is known: 32 bytes for two parts of 16
-            vp[(j / 32 * kTile + i) * 4 + j % 32 / 8] = __builtin_bit_cast(Eight<W>, f4{v[0], v[1], v[2], v[3]});
-            vp[((KS + j / 32) * kTile + i) * 4 + j % 32 / 8] = __builtin_bit_cast(Eight<W>, f4{v[4], v[5], v[6], v[7]});
+            vp[(j / 4 * kTile + i) * 4 + j % 4] = __builtin_bit_cast(Eight<W>, f4{v[0], v[1], v[2], v[3]});
+            vp[((KS + j / 4) * kTile + i) * 4 + j % 4] = __builtin_bit_cast(Eight<W>, f4{v[4], v[5], v[6], v[7]});
+        } else {
+            bf8 part[kParts];
+            split<kParts>(v, part);
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) vp[((p * KS + j / 4) * kTile + i) * 4 + j % 4] = part[p];
         }
-        __syncthreads();
-        for (int u = t; u < tokens * eights; u += kThreads) {
-            const int i = u / eights, j = u % eights * 8;
-            const int at0 = (j / 32 * kTile + i) * 4 + j % 32 / 8, at1 = ((KS + j / 32) * kTile + i) * 4 + j % 32 / 8;
+    };
+    const auto add = [&](int u, int first, int step) {
+        const int i = u / all, j = u % all;
+        Eight<float> v = {};
+        if (i < cnt && j < eights) {
+            const float *p = parts + list[i] * a.R + j * 8;
+#pragma unroll 4
+            for (int s = first; s < splits; s += step) v += load8(p + s * range);
+        }
+        return v;
+    };
+    const int entries = tokens * all, bits = 32 - __builtin_clz(cnt * all - 1), wide = 1 << bits;  // cnt * all and more
+    int share = 1;
+    while (share < splits && 2 * share * wide <= kThreads) share *= 2;
+    if (share > 1) {
+        if (t < share * wide) some[t] = add(t % wide, t >> bits, share);
+        lds_barrier();
+        if (t < entries) {
+            Eight<float> v = {};
+            if (t < wide)
+#pragma unroll 1
+                for (int p = 0; p < share; ++p) v += some[p * wide + t];
+            put(t, v);
+        }
+#pragma unroll 1
+        for (int u = t + kThreads; u < entries; u += kThreads) put(u, Eight<float>{});
+    } else {
+#pragma unroll 1
+        for (int u = t; u < entries; u += kThreads) put(u, add(u, 0, 1));
+    }
+    if constexpr (Held<W, P>::kScaled) {
+        // the largest finite entry of each row goes to [2^14, 2^15): two fp16 parts then hold 22 bits of it, and
+        // of smaller entries all that lies above 2^-38 of it
+        lds_barrier();
+#pragma unroll 1
+        for (int u = t; u < entries; u += kThreads) {
+            const int i = u / all, j = u % all;
+            const int at0 = (j / 4 * kTile + i) * 4 + j % 4, at1 = ((KS + j / 4) * kTile + i) * 4 + j % 4;
             const f4 lo = __builtin_bit_cast(f4, vp[at0]), hi = __builtin_bit_cast(f4, vp[at1]);
             const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
             const int shift = top[i] ? 14 - ((int)(top[i] >> 23) - 127) : 0;  // subnormal rows count as 2^-127
@@ -407,18 +690,8 @@ __device__ __forceinline__ void stage_v(const LoraArgs &a, int64_t slab, int ran
             vp[at1] = p1;
             if (j == 0) undo[i] = ldexpf(1.0f, -shift);
         }
-    } else {
-        for (int u = t; u < tokens * eights; u += kThreads) {
-            const int i = u / eights, j = u % eights * 8;
-            float v[8];
-            sum(i, j, v);
-            bf8 part[kParts];
-            split<kParts>(v, part);
-#pragma unroll
-            for (int p = 0; p < kParts; ++p) vp[((p * KS + j / 32) * kTile + i) * 4 + j % 32 / 8] = part[p];
-        }
     }
-    __syncthreads();
+    lds_barrier();
 }
 
 // Columns [n0, n1) of cnt rows in list, from base to out, 16 bytes a thread.
@@ -440,80 +713,76 @@ __device__ __forceinline__ void copy_rows(const LoraArgs &a, int64_t row0, int c
     }
 }
 
-// A fixed grid walks the units in equal runs: unit (group, kUnit columns), columns fastest, so that a workgroup stages
-// a group's v once for all its columns, and tiles of few and of many groups cost what their work costs.
+// A fixed grid walks units (group, kUnit columns) in runs, columns fastest, so that a workgroup stages a group's v once
+// for all its columns, and tiles of few and of many groups cost what their work costs.
 template <typename W, typename T, int P, int KS>
-__global__ __launch_bounds__(kThreads, KS > 4 ? 1 : kExpandBlocks) void lora_expand_kernel(const LoraArgs a, int64_t m0, int rows, int splits) {
+__global__ __launch_bounds__(kThreads, KS > 4 ? 1 : kExpandBlocks) void lora_expand_kernel(const LoraArgs a, int64_t m0, int rows) {
     __shared__ Eight<W> vp[Held<W, P>::kParts * KS * kTile * 4];
     __shared__ float undo[kTile];
     __shared__ uint32_t top[kTile];
+    __shared__ Eight<float> some[kThreads];
     __shared__ uint8_t list[kTile];
-    const int lane = threadIdx.x % kWave, tiles = (rows + kTile - 1) / kTile;
-    // groups before each lane's tiles; a lane has kCounts / 64 tiles at most
-    const int mine = (tiles + kWave - 1) / kWave;
-    const int *counts = (const int *)a.ws;
-    int upto = 0;
-    for (int i = 0; i < mine; ++i)
-        if (lane * mine + i < tiles) upto += counts[lane * mine + i];
-    for (int o = 1; o < kWave; o <<= 1) {
-        const int v = __shfl_up(upto, o, kWave);
-        if (lane >= o) upto += v;
+    const Head *h = head_of(a);
+    const int splits = __builtin_amdgcn_readfirstlane(h->splits);
+    const int groups = __builtin_amdgcn_readfirstlane(h->groups + h->copies);
+    if (groups == 0) return;
+    // Up to as many groups as workgroups: as many workgroups for each, which meet one group only.  Otherwise runs over all
+    // units; fewer than 2^32, as N <= 2^23 and 512 tiles have 65 groups each at most.
+    const uint32_t per = (uint32_t)((a.N + kUnit - 1) / kUnit);
+    uint32_t u, u1;
+    int k;
+    if ((uint32_t)groups <= gridDim.x) {
+        int rest, part, more;
+        const int share = min(quotient(gridDim.x, groups, rest), (int)per);
+        k = quotient(blockIdx.x, share, part);
+        if (k >= groups) return;
+        const int each = quotient(per, share, more);
+        u = (uint32_t)k * per + each * part + min(part, more);
+        u1 = u + each + (part < more ? 1 : 0);
+    } else {
+        const uint32_t total = per * groups, each = total / gridDim.x, more = total % gridDim.x;
+        u = each * blockIdx.x + min(blockIdx.x, more);
+        u1 = u + each + (blockIdx.x < more ? 1 : 0);
+        k = (int)(u / per);
     }
-    const int64_t per = (a.N + kUnit - 1) / kUnit, total = per * __builtin_amdgcn_readlane(upto, kWave - 1);
-    const int64_t u1 = total * (blockIdx.x + 1) / gridDim.x;
-    for (int64_t u = total * blockIdx.x / gridDim.x; u < u1;) {
-        const int group = (int)(u / per);
-        const int64_t first = u - group * per, last = first + (u1 - u) < per ? first + (u1 - u) : per;
-        u += last - first;
+    for (; u < u1; ++k) {
+        const uint32_t start = u - (uint32_t)k * per;
+        const int64_t first = start, last = start + min(u1 - u, per - start);
+        u += (uint32_t)(last - first);
         const int64_t n0 = first * kUnit, n1 = last * kUnit < a.N ? last * kUnit : a.N;
-        // the group's tile, and its number there
-        const int l = __builtin_ctzll(__ballot(upto > group));
-        int k = group - (l ? __builtin_amdgcn_readlane(upto, l - 1) : 0), tile = l * mine;
-        while (k >= counts[tile]) k -= counts[tile++];
-        const int row = tile * kTile + lane;
-        const int id = row < rows ? a.row_adapter[m0 + row] : -1;
+        const Group g = table_of(a)[k];
+        const int tile = __builtin_amdgcn_readfirstlane(g.tile), ad = __builtin_amdgcn_readfirstlane(g.adapter);
+        const int rank = __builtin_amdgcn_readfirstlane(g.rank), cnt = __builtin_amdgcn_readfirstlane(__popcll(g.mask));
         const int64_t slab = (int64_t)tile * kTile, row0 = m0 + slab;
-        uint64_t left = __ballot((uint32_t)id < (uint32_t)a.L), mask = __ballot(row < rows) & ~left;
-        int ad = -1, rank = 0;
-        if (left) {
-            const uint64_t bare = mask;
-            for (; k >= 0 && left; --k) mask = next_group(id, left, ad);
-            if (k < 0) rank = rank_of(a, ad);
-            else mask = bare;
-        }
         if (rank == 0 && a.base == a.out) continue;
-        gather_rows(mask, list);
-        const int cnt = __popcll(mask);
+        gather_rows(g.mask, list);
         if (rank == 0) {
             copy_rows<T>(a, row0, cnt, list, n0, n1);
             continue;
         }
-        stage_v<W, P, KS>(a, slab, rank, cnt, list, rows, splits, vp, undo, top);
-        if (cnt <= 16) expand_group<W, T, P, KS, 1>(a, row0, ad, rank, cnt, list, vp, undo, n0, n1);
-        else if (cnt <= 32) expand_group<W, T, P, KS, 2>(a, row0, ad, rank, cnt, list, vp, undo, n0, n1);
-        else expand_group<W, T, P, KS, 4>(a, row0, ad, rank, cnt, list, vp, undo, n0, n1);
+        const auto stage = [&] { stage_v<W, P, KS>(a, slab, rank, cnt, list, rows, splits, vp, undo, top, some); };
+        if (cnt <= 16) expand_group<W, T, P, KS, 1>(a, row0, ad, rank, g.scale, cnt, list, vp, undo, n0, n1, stage);
+        else if (cnt <= 32) expand_group<W, T, P, KS, 2>(a, row0, ad, rank, g.scale, cnt, list, vp, undo, n0, n1, stage);
+        else expand_group<W, T, P, KS, 4>(a, row0, ad, rank, g.scale, cnt, list, vp, undo, n0, n1, stage);
     }
 }
 
 // ------------------------------------------------------------------ launches
-struct Plan {
-    int turns, splits, per;  // workgroups that share a tile's adapters; ranges of k, and windows of each
-};
-Plan plan_of(int64_t rows, int64_t K, int32_t L, int32_t R) {
+// the most ranges of k that there can be (Ranges): with one group a tile, and a window a wave or more
+int most_splits(int64_t rows, int64_t K) {
     const int64_t tiles = (rows + kTile - 1) / kTile, windows = (K + kWindow - 1) / kWindow;
-    Plan p;
-    const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(1024 / tiles, (windows + kWaves - 1) / kWaves));
-    p.per = (int)((windows + splits - 1) / splits);
-    p.splits = (int)((windows + p.per - 1) / p.per);
-    p.turns = (int)std::max<int64_t>(1, std::min<int64_t>({kTile, rows, L, 2048 / (tiles * p.splits)}));
-    return p;
+    return (int)std::max<int64_t>(1, std::min(std::max<int64_t>(4, kTarget / tiles), windows / kShrinkWaves));
 }
 
 template <typename X, typename W, int P>
-void shrink(const LoraArgs &a, int64_t m0, int rows, const Plan &p, hipStream_t stream) {
-    const int rt = a.R <= 16 ? 1 : a.R <= 32 ? 2 : 4;
-    const dim3 grid((rows + kTile - 1) / kTile, p.turns * p.splits, (a.R + rt * 16 - 1) / (rt * 16));
-#define W4A8_SHRINK(RT) lora_shrink_kernel<X, W, P, RT><<<grid, kThreads, 0, stream>>>(a, m0, rows, p.turns, p.per)
+void shrink(const LoraArgs &a, int64_t m0, int rows, hipStream_t stream) {
+    const int rt = a.R <= 16 ? 1 : a.R <= 32 ? 2 : 4, most = most_splits(rows, a.K);
+    const int64_t tiles = (rows + kTile - 1) / kTile;
+    const int64_t units = tiles * std::min<int64_t>({kTile, rows, a.L}) * blocks_of(a.R) * most;
+    const uint32_t grid = (uint32_t)std::min<int64_t>(units, kTarget);
+#define W4A8_SHRINK(RT)                                                                                            \
+    (tiles > kSelf ? lora_shrink_kernel<X, W, P, RT, false><<<grid, kShrinkThreads, 0, stream>>>(a, m0, rows, most) \
+                   : lora_shrink_kernel<X, W, P, RT, true><<<grid, kShrinkThreads, 0, stream>>>(a, m0, rows, most))
     if (rt == 1) W4A8_SHRINK(1);
     else if (rt == 2) W4A8_SHRINK(2);
     else W4A8_SHRINK(4);
@@ -521,12 +790,12 @@ void shrink(const LoraArgs &a, int64_t m0, int rows, const Plan &p, hipStream_t 
 }
 
 template <typename W, typename T, int P>
-void expand(const LoraArgs &a, int64_t m0, int rows, const Plan &p, hipStream_t stream) {
+void expand(const LoraArgs &a, int64_t m0, int rows, hipStream_t stream) {
     const int64_t tiles = (rows + kTile - 1) / kTile;
     // no more workgroups than there can be units, or than are resident
-    const int64_t most = tiles * std::min<int64_t>({kTile, rows, (int64_t)a.L + 1}) * ((a.N + kUnit - 1) / kUnit);
-    const uint32_t grid = (uint32_t)std::min<int64_t>(most, 256 * kExpandBlocks);
-#define W4A8_EXPAND(KS) lora_expand_kernel<W, T, P, KS><<<grid, kThreads, 0, stream>>>(a, m0, rows, p.splits)
+    const int64_t units = tiles * std::min<int64_t>({kTile, rows, (int64_t)a.L + 1}) * ((a.N + kUnit - 1) / kUnit);
+    const uint32_t grid = (uint32_t)std::min<int64_t>(units, 256 * kExpandBlocks);
+#define W4A8_EXPAND(KS) lora_expand_kernel<W, T, P, KS><<<grid, kThreads, 0, stream>>>(a, m0, rows)
     if (a.R <= 32) W4A8_EXPAND(1);
     else if (a.R <= 64) W4A8_EXPAND(2);
     else if (a.R <= 128) W4A8_EXPAND(4);
@@ -538,13 +807,14 @@ template <typename W, int P>
 hipError_t launch_w(const LoraArgs &a, hipStream_t stream) {
     for (int64_t m0 = 0; m0 < a.M; m0 += kSlab) {
         const int rows = (int)std::min(a.M - m0, kSlab);
-        const Plan p = plan_of(rows, a.K, a.L, a.R);
-        if (a.x_type == W4A8_F32) shrink<float, W, P>(a, m0, rows, p, stream);
-        else if (a.x_type == W4A8_F16) shrink<_Float16, W, 2>(a, m0, rows, p, stream);
-        else shrink<__bf16, W, 2>(a, m0, rows, p, stream);
-        if (a.out_type == W4A8_F32) expand<W, float, 3>(a, m0, rows, p, stream);
-        else if (a.out_type == W4A8_F16) expand<W, _Float16, 2>(a, m0, rows, p, stream);
-        else expand<W, __bf16, 2>(a, m0, rows, p, stream);
+        if (tiles_in(rows) > kSelf)
+            lora_table_kernel<<<1, kTableThreads, 0, stream>>>(a, m0, rows, most_splits(rows, a.K));
+        if (a.x_type == W4A8_F32) shrink<float, W, P>(a, m0, rows, stream);
+        else if (a.x_type == W4A8_F16) shrink<_Float16, W, 2>(a, m0, rows, stream);
+        else shrink<__bf16, W, 2>(a, m0, rows, stream);
+        if (a.out_type == W4A8_F32) expand<W, float, 3>(a, m0, rows, stream);
+        else if (a.out_type == W4A8_F16) expand<W, _Float16, 2>(a, m0, rows, stream);
+        else expand<W, __bf16, 2>(a, m0, rows, stream);
         if (hipError_t err = hipGetLastError(); err != hipSuccess) return err;
     }
     return hipSuccess;
@@ -554,13 +824,12 @@ hipError_t launch_w(const LoraArgs &a, hipStream_t stream) {
 
 namespace w4a8 {
 
-int64_t lora_ws_bytes(int64_t M, int64_t K, int32_t L, int32_t R) {
+int64_t lora_ws_bytes(int64_t M, int64_t K, int32_t, int32_t R) {
     if (M == 0) return 0;
     // the first slab is the largest, a last and shorter one may have more ranges of k
+    const auto need = [&](int64_t rows) { return parts_at((int)rows) + most_splits(rows, K) * rows * R * 4; };
     const int64_t first = std::min(M, kSlab), last = M % kSlab;
-    int64_t need = plan_of(first, K, L, R).splits * first;
-    if (last) need = std::max(need, plan_of(last, K, L, R).splits * last);
-    return (need * R + kCounts) * 4;
+    return std::max(need(first), last ? need(last) : 0);
 }
 
 hipError_t launch_lora_add(const LoraArgs &a, hipStream_t stream) {
