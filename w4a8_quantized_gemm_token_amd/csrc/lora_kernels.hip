@@ -160,12 +160,9 @@ struct Tile {
             leaders = __ballot((valid >> lane & 1) && __builtin_ctzll(same) == lane);
         }
     }
+    __device__ __forceinline__ Tile(int id, int32_t L, uint64_t leaders)
+        : id(id), valid(__ballot((uint32_t)id < (uint32_t)L)), leaders(leaders) {}
     __device__ __forceinline__ int groups() const { return __popcll(leaders); }
-    // the first lane of group k
-    __device__ __forceinline__ int leader(int k) const {
-        const int lane = threadIdx.x % kWave;
-        return __builtin_ctzll(__ballot((leaders >> lane & 1) && __popcll(leaders & ((1ull << lane) - 1)) == k));
-    }
 };
 
 __device__ __forceinline__ int rank_of(const LoraArgs &a, int id) {
@@ -193,7 +190,7 @@ struct Head {
     int32_t groups, copies, splits, per;  // per: windows of a range of k
     int32_t pad[12];
 };
-constexpr int kSelf = 8;  // up to this many tiles the shrink product finds the groups for itself, a wave a tile
+constexpr int kSelf = 64;  // up to this many tiles the shrink product finds the groups for itself
 
 __host__ __device__ constexpr int tiles_in(int rows) { return (rows + kTile - 1) / kTile; }
 __host__ __device__ constexpr int64_t parts_at(int rows) {
@@ -203,19 +200,39 @@ __device__ __forceinline__ Head *head_of(const LoraArgs &a) { return (Head *)a.w
 __device__ __forceinline__ Group *table_of(const LoraArgs &a) { return (Group *)((Head *)a.ws + 1); }
 __device__ __forceinline__ float *parts_of(const LoraArgs &a, int rows) { return (float *)((char *)a.ws + parts_at(rows)); }
 
-// A tile's entries, its groups from number `at` on and its rows without an adapter at `bare`; every lane calls it.
-__device__ __forceinline__ void write_groups(const LoraArgs &a, const Tile &t, uint64_t in, int tile, int at, int bare) {
+// Entries of N tiles, their groups from number at[] on and their rows without an adapter at bare[]; by whole waves.  All
+// masks first, then all ranks and scales, then the stores, so that a tile does not wait for the last one's loads.
+template <int N>
+__device__ __forceinline__ void write_groups(const LoraArgs &a, const Tile (&t)[N], int rows, const int (&tile)[N],
+                                             const int (&at)[N], const int (&bare)[N]) {
     const int lane = threadIdx.x % kWave;
-    uint64_t mask = 0, left = t.leaders;
-    for (; left; left &= left - 1) {
-        const int first = __builtin_ctzll(left);
-        const uint64_t m = __ballot(t.id == __builtin_amdgcn_readlane(t.id, first)) & t.valid;
-        mask = lane == first ? m : mask;
+    uint64_t mask[N], in[N];
+    int rank[N];
+    float scale[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        mask[i] = 0;
+        in[i] = __ballot(tile[i] * kTile + lane < rows);
+        for (uint64_t left = t[i].leaders; left; left &= left - 1) {
+            const int first = __builtin_ctzll(left);
+            const uint64_t m = __ballot(t[i].id == __builtin_amdgcn_readlane(t[i].id, first)) & t[i].valid;
+            mask[i] = lane == first ? m : mask[i];
+        }
     }
-    if (t.leaders >> lane & 1)
-        table_of(a)[at + __popcll(t.leaders & ((1ull << lane) - 1))] =
-            Group{mask, t.id, rank_of(a, t.id), tile, a.scale ? a.scale[t.id] : 1.0f, {0, 0}};
-    if (a.base != a.out && in != t.valid && lane == 0) table_of(a)[bare] = Group{in & ~t.valid, -1, 0, tile, 0.0f, {0, 0}};
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int id = t[i].leaders >> lane & 1 ? t[i].id : 0;
+        rank[i] = rank_of(a, id);
+        scale[i] = a.scale ? a.scale[id] : 1.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (t[i].leaders >> lane & 1)
+            table_of(a)[at[i] + __popcll(t[i].leaders & ((1ull << lane) - 1))] =
+                Group{mask[i], t[i].id, rank[i], tile[i], scale[i], {0, 0}};
+        if (a.base != a.out && in[i] != t[i].valid && lane == 0)
+            table_of(a)[bare[i]] = Group{in[i] & ~t[i].valid, -1, 0, tile[i], 0.0f, {0, 0}};
+    }
 }
 
 // Ranges of k, and windows of each: as many as make kTarget units of all groups and blocks of ranks, or four where there
@@ -251,23 +268,27 @@ __global__ __launch_bounds__(kTableThreads) void lora_table_kernel(const LoraArg
     const int lane = threadIdx.x % kWave, wave = wave_id(), tiles = tiles_in(rows);
     for (int pass = 0; pass < 2; ++pass) {
         for (int t0 = wave; t0 < tiles; t0 += 4 * kTableWaves) {
-            int id[4];  // under way together
+            int id[4], tile[4], at[4], rest[4];  // four tiles under way together
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int row = (t0 + i * kTableWaves) * kTile + lane;
+                tile[i] = t0 + i * kTableWaves;
+                const int row = tile[i] * kTile + lane;
                 id[i] = row < rows ? a.row_adapter[m0 + row] : -1;
+                at[i] = tile[i] < tiles ? counts[tile[i]] : 0;
+                rest[i] = tile[i] < tiles ? bare[tile[i]] : 0;
             }
+            const Tile t[4] = {Tile(id[0], a.L, ids[wave]), Tile(id[1], a.L, ids[wave]), Tile(id[2], a.L, ids[wave]),
+                               Tile(id[3], a.L, ids[wave])};
+            if (pass) {
+                write_groups<4>(a, t, rows, tile, at, rest);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int tile = t0 + i * kTableWaves;
-                if (tile >= tiles) break;
-                const Tile t(id[i], a.L, ids[wave]);
-                const uint64_t in = __ballot(tile * kTile + lane < rows);
-                if (pass) {
-                    write_groups(a, t, in, tile, counts[tile], bare[tile]);
-                } else if (lane == 0) {
-                    counts[tile] = t.groups();
-                    bare[tile] = a.base != a.out && in != t.valid ? 1 : 0;
+                for (int i = 0; i < 4; ++i) {
+                    const uint64_t in = __ballot(tile[i] * kTile + lane < rows);
+                    if (lane == 0 && tile[i] < tiles) {
+                        counts[tile[i]] = t[i].groups();
+                        bare[tile[i]] = a.base != a.out && in != t[i].valid ? 1 : 0;
+                    }
                 }
             }
         }
@@ -303,9 +324,13 @@ __global__ __launch_bounds__(kTableThreads) void lora_table_kernel(const LoraArg
 // ------------------------------------------------------------------ shrink
 // v[token][j] over windows [w0, w1) of k for cnt rows in list and 16 RT ranks from j0; waves take windows in turn.
 // Matrix rows are ranks, matrix columns tokens.
+// Matrix tiles of a round of adding the waves' sums up.
+template <int RT>
+constexpr int kRound = RT == 1 ? 4 : 8;
+
 template <typename X, typename W, int P, int TT, int RT>
 __device__ __forceinline__ void shrink_group(const LoraArgs &a, int64_t row0, int64_t slab, int id, int rank, int j0, int cnt,
-                                             const uint8_t *list, int w0, int w1, float *part, f4 (*red)[RT][kWave]) {
+                                             const uint8_t *list, int w0, int w1, float *part, f4 (*red)[kRound<RT>][kWave]) {
     using OX = Operand<X, W, P>;
     using OW = Operand<W, X, P>;
     const int wave = wave_id(), lane = threadIdx.x % kWave, col = lane % 16, g = lane / 16;
@@ -369,20 +394,23 @@ __device__ __forceinline__ void shrink_group(const LoraArgs &a, int64_t row0, in
         }
         step(rw, rx);
     }
-    // the waves' sums together, and to the workspace: lane has ranks 4 g .. 4 g + 3 of its tile, token col
+    // the waves' sums together, a round of matrix tiles at a time and one wave for each, and to the workspace: lane has
+    // ranks 4 g .. 4 g + 3 of the tile, token col
+    constexpr int kTiles = TT * RT, kStep = kRound<RT> < kTiles ? kRound<RT> : kTiles;
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-        if (t) lds_barrier();
+    for (int m = 0; m < kTiles; m += kStep) {
+        if (m) lds_barrier();
 #pragma unroll
-        for (int r = 0; r < RT; ++r) red[wave][r][lane] = acc[t][r];
+        for (int i = 0; i < kStep; ++i) red[wave][i][lane] = acc[(m + i) / RT][(m + i) % RT];
         lds_barrier();
-        const int i = t * 16 + col;
-        for (int r = wave; r < RT; r += kShrinkWaves) {
-            const int j = j0 + r * 16 + 4 * g;
-            f4 s = red[0][r][lane];
+        if (wave < kStep) {
+            const int i = (m + wave) / RT * 16 + col, j = j0 + (m + wave) % RT * 16 + 4 * g;
+            f4 v[kShrinkWaves];
 #pragma unroll
-            for (int w = 1; w < kShrinkWaves; ++w) s += red[w][r][lane];
-            if (i < cnt && j < a.R) *reinterpret_cast<f4 *>(part + (slab + list[i]) * a.R + j) = s;
+            for (int w = 0; w < kShrinkWaves; ++w) v[w] = red[w][wave][lane];
+#pragma unroll
+            for (int w = 1; w < kShrinkWaves; ++w) v[0] += v[w];
+            if (i < cnt && j < a.R) *reinterpret_cast<f4 *>(part + (slab + list[i]) * a.R + j) = v[0];
         }
     }
 }
@@ -391,43 +419,51 @@ __device__ __forceinline__ void shrink_group(const LoraArgs &a, int64_t row0, in
 // writes the table for the expand product.
 template <typename X, typename W, int P, int RT, bool SELF>
 __global__ __launch_bounds__(kShrinkThreads) void lora_shrink_kernel(const LoraArgs a, int64_t m0, int rows, int most) {
-    __shared__ f4 red[kShrinkWaves][RT][kWave];
-    __shared__ __attribute__((aligned(16))) int ids[kShrinkWaves][kWave];
+    __shared__ f4 red[kShrinkWaves][kRound<RT>][kWave];
+    __shared__ __attribute__((aligned(16))) int ids[SELF ? kSelf : 1][kWave];  // of all tiles
     __shared__ uint64_t masks[kSelf];
     __shared__ int counts[2][kSelf];
     __shared__ uint8_t list[kTile];
     const int lane = threadIdx.x % kWave, wave = wave_id(), tiles = tiles_in(rows);
     const int windows = (int)((a.K + kWindow - 1) / kWindow), blocks = blocks_of(a.R);
     Head h;
-    int id = -1;
+    int upto = 0;  // groups up to and with tile `lane`
     if (SELF) {
-        const int row = wave * kTile + lane;
-        id = row < rows ? a.row_adapter[m0 + row] : -1;
-        const Tile t(id, a.L, ids[wave]);
-        const uint64_t in = __ballot(row < rows);
-        if (lane == 0) {
-            counts[0][wave] = t.groups();
-            counts[1][wave] = a.base != a.out && in != t.valid ? 1 : 0;
+        constexpr int kMine = kSelf / kShrinkWaves;  // a wave's tiles, all their ids under way together
+        int id[kMine];
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int row = (i * kShrinkWaves + wave) * kTile + lane;
+            id[i] = row < rows ? a.row_adapter[m0 + row] : -1;
         }
-        ids[wave][lane] = id;
-        if (lane == 0) masks[wave] = t.leaders;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int tile = i * kShrinkWaves + wave;
+            if (tile >= tiles) break;
+            const Tile t(id[i], a.L, ids[tile]);
+            const uint64_t in = __ballot(tile * kTile + lane < rows);
+            ids[tile][lane] = id[i];
+            if (lane == 0) {
+                counts[0][tile] = t.groups();
+                counts[1][tile] = a.base != a.out && in != t.valid ? 1 : 0;
+                masks[tile] = t.leaders;
+            }
+        }
         lds_barrier();
-        const int c = lane < kSelf ? counts[0][lane] : 0, b = lane < kSelf ? counts[1][lane] : 0;
-        const int cs = sum_upto(c), bs = sum_upto(b);
-        h.groups = __builtin_amdgcn_readlane(cs, kWave - 1);
+        const int c = lane < tiles ? counts[0][lane] : 0, b = lane < tiles ? counts[1][lane] : 0;
+        const int bs = sum_upto(b);
+        upto = sum_upto(c);
+        h.groups = __builtin_amdgcn_readlane(upto, kWave - 1);
         h.copies = __builtin_amdgcn_readlane(bs, kWave - 1);
         set_ranges(h, rows, a.K, a.R, most);
-        if (blockIdx.x == 0) {
-            if (threadIdx.x == 0) {
-                head_of(a)->groups = h.groups;
-                head_of(a)->copies = h.copies;
-                head_of(a)->splits = h.splits;
+        if (blockIdx.x == gridDim.x - 1) {
+            if (threadIdx.x == 0) *head_of(a) = Head{h.groups, h.copies, h.splits, h.per, {}};
+            for (int tile = wave; tile < tiles; tile += kShrinkWaves) {
+                const Tile t[1] = {Tile(ids[tile][lane], a.L, masks[tile])};
+                write_groups<1>(a, t, rows, {tile}, {__builtin_amdgcn_readlane(upto - c, tile)},
+                                {h.groups + __builtin_amdgcn_readlane(bs - b, tile)});
             }
-            if (wave < tiles)
-                write_groups(a, t, in, wave, __builtin_amdgcn_readlane(cs - c, wave),
-                             h.groups + __builtin_amdgcn_readlane(bs - b, wave));
         }
-        id = cs;  // groups up to and with tile `lane`, for the search below
     } else {
         h.groups = head_of(a)->groups;
         h.splits = head_of(a)->splits;
@@ -439,8 +475,8 @@ __global__ __launch_bounds__(kShrinkThreads) void lora_shrink_kernel(const LoraA
         const int j0 = block * 16 * RT;
         Group g;
         if (SELF) {
-            g.tile = __builtin_ctzll(__ballot(id > k));
-            if (g.tile) k -= __builtin_amdgcn_readlane(id, g.tile - 1);
+            g.tile = __builtin_ctzll(__ballot(upto > k));
+            if (g.tile) k -= __builtin_amdgcn_readlane(upto, g.tile - 1);
             const uint64_t leaders = masks[g.tile];
             const int mine = ids[g.tile][lane];
             const int first =
@@ -644,7 +680,7 @@ __device__ __forceinline__ void stage_v(const LoraArgs &a, int64_t slab, int ran
         Eight<float> v = {};
         if (i < cnt && j < eights) {
             const float *p = parts + list[i] * a.R + j * 8;
-#pragma unroll 4
+#pragma unroll 8
             for (int s = first; s < splits; s += step) v += load8(p + s * range);
         }
         return v;
@@ -792,9 +828,11 @@ void shrink(const LoraArgs &a, int64_t m0, int rows, hipStream_t stream) {
 template <typename W, typename T, int P>
 void expand(const LoraArgs &a, int64_t m0, int rows, hipStream_t stream) {
     const int64_t tiles = (rows + kTile - 1) / kTile;
-    // no more workgroups than there can be units, or than are resident
+    // no more workgroups than there can be units; as many as are resident, or where those would have long runs each, more
+    // of shorter ones (long prefill 566 us with 46 units each, 515 with 12; prefill 92 us with 5 units each, 96 with 3)
     const int64_t units = tiles * std::min<int64_t>({kTile, rows, (int64_t)a.L + 1}) * ((a.N + kUnit - 1) / kUnit);
-    const uint32_t grid = (uint32_t)std::min<int64_t>(units, 256 * kExpandBlocks);
+    const int64_t runs = tiles * ((a.N + kUnit - 1) / kUnit) / 12;
+    const uint32_t grid = (uint32_t)std::min<int64_t>(units, std::max<int64_t>(256 * kExpandBlocks, std::min<int64_t>(runs, 1 << 20)));
 #define W4A8_EXPAND(KS) lora_expand_kernel<W, T, P, KS><<<grid, kThreads, 0, stream>>>(a, m0, rows)
     if (a.R <= 32) W4A8_EXPAND(1);
     else if (a.R <= 64) W4A8_EXPAND(2);
