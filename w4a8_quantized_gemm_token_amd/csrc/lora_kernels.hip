@@ -200,6 +200,20 @@ __device__ __forceinline__ Head *head_of(const LoraArgs &a) { return (Head *)a.w
 __device__ __forceinline__ Group *table_of(const LoraArgs &a) { return (Group *)((Head *)a.ws + 1); }
 __device__ __forceinline__ float *parts_of(const LoraArgs &a, int rows) { return (float *)((char *)a.ws + parts_at(rows)); }
 
+// Entry k, the same in every lane.  What it holds is cut to the call's sizes: whatever the memory holds, no row, adapter or
+// rank outside them is met.
+__device__ __forceinline__ Group group_of(const LoraArgs &a, int rows, int k) {
+    Group g = table_of(a)[k];
+    g.tile = min((uint32_t)__builtin_amdgcn_readfirstlane(g.tile), (uint32_t)tiles_in(rows) - 1);
+    g.adapter = __builtin_amdgcn_readfirstlane(g.adapter);
+    g.rank = (uint32_t)g.adapter < (uint32_t)a.L ? min((uint32_t)__builtin_amdgcn_readfirstlane(g.rank), (uint32_t)a.R) : 0;
+    const int in = rows - g.tile * kTile;
+    const uint64_t mask = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(g.mask >> 32)) << 32 |
+                          (uint32_t)__builtin_amdgcn_readfirstlane((int)g.mask);
+    g.mask = in < kTile ? mask & ((1ull << in) - 1) : mask;
+    return g;
+}
+
 // Entries of N tiles, their groups from number at[] on and their rows without an adapter at bare[]; by whole waves.  All
 // masks first, then all ranks and scales, then the stores, so that a tile does not wait for the last one's loads.
 template <int N>
@@ -465,8 +479,8 @@ __global__ __launch_bounds__(kShrinkThreads) void lora_shrink_kernel(const LoraA
             }
         }
     } else {
-        h.groups = head_of(a)->groups;
-        h.splits = head_of(a)->splits;
+        h.groups = min((uint32_t)head_of(a)->groups, (uint32_t)tiles * kTile);
+        h.splits = min((uint32_t)head_of(a)->splits, (uint32_t)most);
         h.per = head_of(a)->per;
     }
     for (int u = blockIdx.x; u < h.groups * blocks * h.splits; u += gridDim.x) {
@@ -483,16 +497,13 @@ __global__ __launch_bounds__(kShrinkThreads) void lora_shrink_kernel(const LoraA
                 __builtin_ctzll(__ballot((leaders >> lane & 1) && __popcll(leaders & ((1ull << lane) - 1)) == k));
             g.adapter = __builtin_amdgcn_readlane(mine, first);
             g.mask = __ballot(mine == g.adapter);
-            g.rank = rank_of(a, g.adapter);
+            g.rank = (uint32_t)g.adapter < (uint32_t)a.L ? rank_of(a, g.adapter) : 0;
         } else {
-            g = table_of(a)[k];
-            g.tile = __builtin_amdgcn_readfirstlane(g.tile);
-            g.adapter = __builtin_amdgcn_readfirstlane(g.adapter);
-            g.rank = __builtin_amdgcn_readfirstlane(g.rank);
+            g = group_of(a, rows, k);
         }
-        if (j0 >= g.rank) continue;
+        if (j0 >= g.rank || !g.mask) continue;
         gather_rows(g.mask, list);
-        const int cnt = __builtin_amdgcn_readfirstlane(__popcll(g.mask));
+        const int cnt = __popcll(g.mask);
         const int64_t slab = (int64_t)g.tile * kTile, row0 = m0 + slab;
         const int w0 = split * h.per, w1 = min(w0 + h.per, windows);
         float *part = parts_of(a, rows) + (int64_t)split * rows * a.R;
@@ -752,15 +763,17 @@ __device__ __forceinline__ void copy_rows(const LoraArgs &a, int64_t row0, int c
 // A fixed grid walks units (group, kUnit columns) in runs, columns fastest, so that a workgroup stages a group's v once
 // for all its columns, and tiles of few and of many groups cost what their work costs.
 template <typename W, typename T, int P, int KS>
-__global__ __launch_bounds__(kThreads, KS > 4 ? 1 : kExpandBlocks) void lora_expand_kernel(const LoraArgs a, int64_t m0, int rows) {
+__global__ __launch_bounds__(kThreads, KS > 4 ? 1 : kExpandBlocks) void lora_expand_kernel(const LoraArgs a, int64_t m0, int rows, int most) {
     __shared__ Eight<W> vp[Held<W, P>::kParts * KS * kTile * 4];
     __shared__ float undo[kTile];
     __shared__ uint32_t top[kTile];
     __shared__ Eight<float> some[kThreads];
     __shared__ uint8_t list[kTile];
     const Head *h = head_of(a);
-    const int splits = __builtin_amdgcn_readfirstlane(h->splits);
-    const int groups = __builtin_amdgcn_readfirstlane(h->groups + h->copies);
+    // (cut to what the workspace holds, as the table's entries are)
+    const int splits = min((uint32_t)__builtin_amdgcn_readfirstlane(h->splits), (uint32_t)most);
+    const int groups = min((uint32_t)__builtin_amdgcn_readfirstlane(h->groups + h->copies),
+                           (uint32_t)tiles_in(rows) * (min(rows, kTile) + 1));
     if (groups == 0) return;
     // Up to as many groups as workgroups: as many workgroups for each, which meet one group only.  Otherwise runs over all
     // units; fewer than 2^32, as N <= 2^23 and 512 tiles have 65 groups each at most.
@@ -786,11 +799,10 @@ __global__ __launch_bounds__(kThreads, KS > 4 ? 1 : kExpandBlocks) void lora_exp
         const int64_t first = start, last = start + min(u1 - u, per - start);
         u += (uint32_t)(last - first);
         const int64_t n0 = first * kUnit, n1 = last * kUnit < a.N ? last * kUnit : a.N;
-        const Group g = table_of(a)[k];
-        const int tile = __builtin_amdgcn_readfirstlane(g.tile), ad = __builtin_amdgcn_readfirstlane(g.adapter);
-        const int rank = __builtin_amdgcn_readfirstlane(g.rank), cnt = __builtin_amdgcn_readfirstlane(__popcll(g.mask));
-        const int64_t slab = (int64_t)tile * kTile, row0 = m0 + slab;
-        if (rank == 0 && a.base == a.out) continue;
+        const Group g = group_of(a, rows, k);
+        const int ad = g.adapter, rank = g.rank, cnt = __popcll(g.mask);
+        const int64_t slab = (int64_t)g.tile * kTile, row0 = m0 + slab;
+        if (!g.mask || (rank == 0 && a.base == a.out)) continue;
         gather_rows(g.mask, list);
         if (rank == 0) {
             copy_rows<T>(a, row0, cnt, list, n0, n1);
@@ -833,7 +845,7 @@ void expand(const LoraArgs &a, int64_t m0, int rows, hipStream_t stream) {
     const int64_t units = tiles * std::min<int64_t>({kTile, rows, (int64_t)a.L + 1}) * ((a.N + kUnit - 1) / kUnit);
     const int64_t runs = tiles * ((a.N + kUnit - 1) / kUnit) / 12;
     const uint32_t grid = (uint32_t)std::min<int64_t>(units, std::max<int64_t>(256 * kExpandBlocks, std::min<int64_t>(runs, 1 << 20)));
-#define W4A8_EXPAND(KS) lora_expand_kernel<W, T, P, KS><<<grid, kThreads, 0, stream>>>(a, m0, rows)
+#define W4A8_EXPAND(KS) lora_expand_kernel<W, T, P, KS><<<grid, kThreads, 0, stream>>>(a, m0, rows, most_splits(rows, a.K))
     if (a.R <= 32) W4A8_EXPAND(1);
     else if (a.R <= 64) W4A8_EXPAND(2);
     else if (a.R <= 128) W4A8_EXPAND(4);

@@ -97,6 +97,9 @@ __device__ __forceinline__ double wave_sum(double v) {
     return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
 }
 
+// A barrier for what passes through LDS.  (__syncthreads would also wait for the stores to memory that are under way.)
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // Sums and maxima over the workgroup.  Two exchange buffers in turn: a wave writes one only after
 // the barrier of the reduction between, which every wave passes after it has read it.
 struct Block {
@@ -108,7 +111,7 @@ struct Block {
         if (waves == 1) return v;
         double *r = red + 16 * (turn ^= 1);
         if (threadIdx.x % kWave == 0) r[threadIdx.x / kWave] = v;
-        __syncthreads();
+        lds_barrier();
         const int i = threadIdx.x % 16;
         return row16_sum(i < waves ? r[i] : 0.0);
     }
@@ -118,7 +121,7 @@ struct Block {
         if (waves == 1) return v;
         float *r = reinterpret_cast<float *>(red + 16 * (turn ^= 1));
         if (threadIdx.x % kWave == 0) r[threadIdx.x / kWave] = v;
-        __syncthreads();
+        lds_barrier();
         const int i = threadIdx.x % 16;
         v = i < waves ? r[i] : 0.0f;
         v = dpp_max<0xB1>(v);
