@@ -234,6 +234,18 @@ def test_larger(M, K, N, R, how):
     Case(M, M, K, N, R, L=6, ids=how, x="bf16", out="f32").check(in_place=True)
 
 
+@pytest.mark.parametrize("M", [511, 513, 4096, 4097, 4161])
+@pytest.mark.parametrize("how", ["sorted", "distinct", "holes"])
+def test_many_tiles(M, how):
+    """Around the numbers of tiles at which the groups are found another way; few and many groups a tile, copied rows."""
+    Case(M, M, 72, 40, 8, L=70, ids=how, x="bf16", out="f32", ranks=np.arange(70) % 9).check()
+
+
+def test_more_groups_than_workgroups():
+    """10000 rows of 64 adapters in turn: ten thousand groups."""
+    Case(1, 10000, 24, 130, 8, L=64, ids="distinct", x="f16", ab="f16", out="bf16").check()
+
+
 def plain(x, ids, A, B, scale, base):
     """The definition in float64 on the device, adapter by adapter."""
     out = base.double()

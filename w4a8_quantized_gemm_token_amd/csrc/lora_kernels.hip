@@ -528,7 +528,10 @@ __device__ __forceinline__ void cut(Eight<W> &x, int n) {
     for (int e = 0; e < 8; ++e) x[e] = e < n ? x[e] : (W)0.0f;
 }
 
-constexpr int kExpandBlocks = 3;  // workgroups a CU
+// Workgroups a CU: three, where the rows of v leave LDS for them.
+constexpr int kExpandBlocks = 3;
+template <typename W, int P, int KS>
+constexpr int kResident = KS > 4 ? 1 : KS == 4 && Held<W, P>::kParts == 3 ? 2 : kExpandBlocks;
 constexpr int kUnit = 128;  // columns that a workgroup's share of a group is counted in
 
 // Columns of a wave's step of NT matrix tiles, dealt so that a lane has 16 bytes of output columns in a row: piece p of the
@@ -763,7 +766,8 @@ __device__ __forceinline__ void copy_rows(const LoraArgs &a, int64_t row0, int c
 // A fixed grid walks units (group, kUnit columns) in runs, columns fastest, so that a workgroup stages a group's v once
 // for all its columns, and tiles of few and of many groups cost what their work costs.
 template <typename W, typename T, int P, int KS>
-__global__ __launch_bounds__(kThreads, KS > 4 ? 1 : kExpandBlocks) void lora_expand_kernel(const LoraArgs a, int64_t m0, int rows, int most) {
+__global__ __launch_bounds__(kThreads, (kResident<W, P, KS>)) void lora_expand_kernel(const LoraArgs a, int64_t m0,
+                                                                                                int rows, int most) {
     __shared__ Eight<W> vp[Held<W, P>::kParts * KS * kTile * 4];
     __shared__ float undo[kTile];
     __shared__ uint32_t top[kTile];
