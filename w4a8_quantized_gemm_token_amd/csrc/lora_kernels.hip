@@ -249,16 +249,21 @@ __device__ __forceinline__ void write_groups(const LoraArgs &a, const Tile (&t)[
     }
 }
 
-// Ranges of k, and windows of each: as many as make kTarget units of all groups and blocks of ranks, or four where there
-// are more units than that already (so that the last round of workgroups is a short one), but no more parts of v than
-// each group's columns are worth reading (kStaged bytes a group on average), and no more than the workspace has room for.
-constexpr int kTarget = 512, kStaged = 65536;
+// Ranges of k, and windows of each.  At least as many as make kFill units (group, block of ranks, range): 978 rows of one
+// adapter of rank 120 with k 5160 take 30 us, 50 without; with 256 units instead 34, and 1656 rows in 156 units 42 instead
+// of 34.  Beyond that up to kTarget units, or four ranges where there are as many units already (so that the last round
+// of workgroups is a short one), if the expand product has not to read more than kStaged bytes of parts of v for a group on
+// average: with twice that the long prefill takes 570 us instead of 529, with half of it the prompts 32.0 instead of 31.3.
+// Never more than the workspace has room for.
+constexpr int kTarget = 512, kFill = 128, kStaged = 65536;
 constexpr int blocks_of(int R) { return R <= 64 ? 1 : (R + 63) / 64; }  // of ranks in the shrink product
 __device__ __forceinline__ void set_ranges(Head &h, int rows, int64_t K, int R, int most) {
     const int windows = (int)((K + kWindow - 1) / kWindow);
     const float units = (float)max(1, h.groups * blocks_of(R));
-    const int worth = max(2, (int)(kStaged / 4 * (float)h.groups * __builtin_amdgcn_rcpf((float)(rows * R))));
-    const int wanted = max(1, min(min(max(4, (int)(kTarget * __builtin_amdgcn_rcpf(units))), worth), most));
+    const float each = __builtin_amdgcn_rcpf(units);
+    const int worth = (int)(kStaged / 4 * (float)h.groups * __builtin_amdgcn_rcpf((float)(rows * R)));
+    const int more = min(max(4, (int)(kTarget * each)), worth);
+    const int wanted = max(1, min(max((int)(kFill * each + 0.99f), more), most));
     int rest;
     h.per = quotient(windows + wanted - 1, wanted, rest);
     h.splits = quotient(windows + h.per - 1, h.per, rest);
@@ -630,26 +635,29 @@ __device__ __forceinline__ void expand_group(const LoraArgs &a, int64_t row0, in
             }
         if (n + kWaves * C::kStep < whole) load(n + kWaves * C::kStep);
     }
-    // the columns at N's end: 16 at a time, element by element, 16 rows a wave
+    // the columns at N's end: 16 at a time, element by element, 16 rows a wave, all loads before the products
     for (int u = wave; whole + u / TT * 16 < n1; u += kWaves) {
         const int i = u % TT * 16 + col;
         const int64_t c = whole + u / TT * 16, nn = c + col < n1 ? c + col : n1 - 1;
-        f4 acc = {};
-        for (int ks = 0; ks * 32 < rank; ++ks) {
-            Eight<W> b = ks * 32 + 8 * g < rank ? load8(pb + nn * a.R + 8 * g + ks * 32) : zero8<W>();
-            cut(b, rank - ks * 32 - 8 * g);
+        const int64_t row = list[i < cnt ? i : 0];
+        Eight<W> b[KS];
+        T old[4];
 #pragma unroll
-            for (int p = 0; p < kParts; ++p) acc = mfma(b, vp[((p * KS + ks) * kTile + i) * 4 + g], acc);
+        for (int ks = 0; ks < KS; ++ks) b[ks] = ks * 32 + 8 * g < rank ? load8(pb + nn * a.R + 8 * g + ks * 32) : zero8<W>();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) old[e] = base[row * a.ldb + (c + 4 * g + e < n1 ? c + 4 * g + e : n1 - 1)];
+        f4 acc = {};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            if (ks * 32 >= rank) break;
+            cut(b[ks], rank - ks * 32 - 8 * g);
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) acc = mfma(b[ks], vp[((p * KS + ks) * kTile + i) * 4 + g], acc);
         }
-        if (i >= cnt) continue;
-        const int64_t row = list[i];
         const float fi = Held<W, P>::kScaled ? scale * undo[i] : scale;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (c + 4 * g + e < n1) {
-                const float have = (float)base[row * a.ldb + c + 4 * g + e];
-                out[row * a.ldo + c + 4 * g + e] = (T)(have + fi * acc[e]);
-            }
+            if (i < cnt && c + 4 * g + e < n1) out[row * a.ldo + c + 4 * g + e] = (T)((float)old[e] + fi * acc[e]);
     }
 }
 
@@ -708,7 +716,7 @@ __device__ __forceinline__ void stage_v(const LoraArgs &a, int64_t slab, int ran
         if (t < entries) {
             Eight<float> v = {};
             if (t < wide)
-#pragma unroll 1
+#pragma unroll 4
                 for (int p = 0; p < share; ++p) v += some[p * wide + t];
             put(t, v);
         }
