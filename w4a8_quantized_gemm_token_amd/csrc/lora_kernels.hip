@@ -1,16 +1,22 @@
 // lora_kernels.hip -- low-rank adapters of many requests beside a shared projection.
 //
 // For row m with adapter a: v = A_a x[m] (rank values), out[m] = base[m] + scale_a B_a v.
-// Two launches: the shrink product leaves parts of v per range of k in the workspace, the expand
-// product adds them up and walks the output.  Both go by tiles of 64 rows as they stand: a wave's
-// lanes hold the 64 adapter ids, the distinct ones are found with ballots, and each one's rows are
-// gathered into 16-row columns of the matrix instruction, so rows of one adapter share its loads
-// without being sorted beforehand, and no row can be met twice.
+// Two launches: the shrink product leaves parts of v per range of k in the workspace, the expand product adds them up
+// and walks the output.  Both go by tiles of 64 rows as they stand: a wave's lanes hold the 64 adapter ids, the distinct
+// ones are found with ballots, and each one's rows (a group) are gathered into 16-row columns of the matrix
+// instruction, so rows of one adapter share its loads without being sorted beforehand, and no row can be met
+// twice.  The groups stand in a table in the workspace, which a workgroup of the shrink product writes, or a launch of
+// its own in front of it above 64 tiles.  Longer calls go by slabs of 32768 rows.
 //
 // Arithmetic: the matrix cores take 16-bit operands.  fp32 values enter as sums of bf16 parts, each
 // the next 8 bits cut off the rest (three hold all 24, two hold 16, which 16-bit outputs do with);
 // an fp16 value beside bf16 is two such parts, exactly.  v meets fp16 weights as two fp16 parts (22
 // bits) after a scaling of its row by a power of two.  All sums are fp32.
+//
+// What has to move: x, base and out once, and the A and B of the adapters in use.  Times and bounds stand at the kernels
+// for these calls (rows; adapters in use; rank; k; columns): one token (1; 1; 16; 7168; 4096), decode batch (64; 48; 16;
+// 8192; 28672), prompts (500; 5; 64; 4096; 14340), prefill (4096; 4; 16; 8192; 8192), long prefill (20011; 3; to 128; 4096;
+// 14336).
 #include "block_internal.hpp"
 
 #include <algorithm>
@@ -121,8 +127,8 @@ struct Operand<_Float16, _Float16, P> {
 };
 
 // ------------------------------------------------------------------ groups of a tile
-// A tile's groups: its distinct valid adapters in the order of their first rows.  A wave finds the k-th one after another
-// (46 ns each), or, from the ninth on, all at once by comparing every pair of ids.
+// A tile's groups: its distinct valid adapters in the order of their first rows.  A wave finds the first eight one after
+// another (46 ns each), and if there are more, all at once by comparing every pair of ids.
 constexpr int kInTurn = 8;
 
 // The lanes that hold this lane's id; every lane calls it.  ids: 64 words of LDS, the wave's own.
@@ -279,7 +285,8 @@ __device__ __forceinline__ int sum_upto(int v) {
     return v + __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
 }
 
-// More tiles: the table by one workgroup, wave w the tiles w, w + 16, ...
+// More tiles: the table by one workgroup, wave w the tiles w, w + 16, ...  Latency of its two passes over the ids: 313
+// tiles take 24 us, in a call of 530.
 constexpr int kTableThreads = 1024, kTableWaves = kTableThreads / kWave, kMaxTiles = kSlab / kTile;
 __global__ __launch_bounds__(kTableThreads) void lora_table_kernel(const LoraArgs a, int64_t m0, int rows, int most) {
     __shared__ __attribute__((aligned(16))) int ids[kTableWaves][kWave];
@@ -341,12 +348,12 @@ __global__ __launch_bounds__(kTableThreads) void lora_table_kernel(const LoraArg
 }
 
 // ------------------------------------------------------------------ shrink
-// v[token][j] over windows [w0, w1) of k for cnt rows in list and 16 RT ranks from j0; waves take windows in turn.
-// Matrix rows are ranks, matrix columns tokens.
 // Matrix tiles of a round of adding the waves' sums up.
 template <int RT>
 constexpr int kRound = RT == 1 ? 4 : 8;
 
+// v[token][j] over windows [w0, w1) of k for cnt rows in list and 16 RT ranks from j0; waves take windows in turn.
+// Matrix rows are ranks, matrix columns tokens.
 template <typename X, typename W, int P, int TT, int RT>
 __device__ __forceinline__ void shrink_group(const LoraArgs &a, int64_t row0, int64_t slab, int id, int rank, int j0, int cnt,
                                              const uint8_t *list, int w0, int w1, float *part, f4 (*red)[kRound<RT>][kWave]) {
@@ -434,8 +441,14 @@ __device__ __forceinline__ void shrink_group(const LoraArgs &a, int64_t row0, in
     }
 }
 
-// A fixed grid walks units (group, block of ranks, range of k).  SELF: every workgroup finds the groups, and the first one
-// writes the table for the expand product.
+// A fixed grid walks units (group, block of ranks, range of k): 16 to 64 ranks (RT matrix tiles) against 16, 32 or 64
+// of the group's rows, eight waves sharing out the range.  One token 4.9 us and decode batch 6.9 us: finding the groups,
+// one or two windows' loads and adding the waves' sums up, one after another.  Prefill 23.6 us, 2.8 TB/s.  Long prefill
+// 178 us: 1.8 TB/s of x, where a window's loads, the cutting of its fp32 values into parts and its products (fp16
+// weights: two parts each) stand one after another in a wave, the other waves of a CU cover only part of that, and the
+// last round of units leaves CUs idle.  Units of 32 rows with twice the waves a CU spilled and were slower; grids of
+// 256 to 2048 take the same time.  SELF: every workgroup finds the groups for itself, and the last one writes the table
+// for the expand product.
 template <typename X, typename W, int P, int RT, bool SELF>
 __global__ __launch_bounds__(kShrinkThreads) void lora_shrink_kernel(const LoraArgs a, int64_t m0, int rows, int most) {
     __shared__ f4 red[kShrinkWaves][kRound<RT>][kWave];
@@ -772,7 +785,11 @@ __device__ __forceinline__ void copy_rows(const LoraArgs &a, int64_t row0, int c
 }
 
 // A fixed grid walks units (group, kUnit columns) in runs, columns fastest, so that a workgroup stages a group's v once
-// for all its columns, and tiles of few and of many groups cost what their work costs.
+// for all its columns, and tiles of few and of many groups cost what their work costs.  Prefill 62 us, 4.4 TB/s of base and
+// output, 5.6 TB/s once all workgroups are past their staging; long prefill 338 us, which is 3.4 TB/s: about 5 TB/s in the
+// loop, staging 64 rows of 128 ranks in front of each run, and groups of large and of small rank side by side.
+// Decode batch 18 us and one token 6 us are latency: the table, the parts of v, and a run of steps whose loads (base and
+// B) are one step ahead.
 template <typename W, typename T, int P, int KS>
 __global__ __launch_bounds__(kThreads, (kResident<W, P, KS>)) void lora_expand_kernel(const LoraArgs a, int64_t m0,
                                                                                                 int rows, int most) {
@@ -828,7 +845,7 @@ __global__ __launch_bounds__(kThreads, (kResident<W, P, KS>)) void lora_expand_k
 }
 
 // ------------------------------------------------------------------ launches
-// the most ranges of k that there can be (Ranges): with one group a tile, and a window a wave or more
+// the most ranges of k that the parts of v have room for: with one group a tile, and a window a wave or more
 int most_splits(int64_t rows, int64_t K) {
     const int64_t tiles = (rows + kTile - 1) / kTile, windows = (K + kWindow - 1) / kWindow;
     return (int)std::max<int64_t>(1, std::min(std::max<int64_t>(4, kTarget / tiles), windows / kShrinkWaves));
