@@ -318,7 +318,8 @@ w4a8_status w4a8_moe_grouped_gemm_w8a8(const int8_t *qa, const float *a_scale, i
  *   or NULL (1), base and out [M][N] of out_type (row strides ldb, ldo; the elements between
  *   rows are not written).  base may be out itself (the same pointer and stride: the term is
  *   added in place and rows without an adapter are not touched); otherwise the two do not
- *   overlap.  Entries of A and B past rank_a are not used, whatever they hold.
+ *   overlap.  No other input overlaps out or the workspace.  Entries of A and B past rank_a are not used, whatever they hold.
+ * Equal calls give equal bytes; the order in which a row's sums are taken may turn on the call's other rows.
  * How exactly the two products take part: x and v enter the matrix cores as sums of 16-bit
  * values that together hold at least 22 bits of each with out_type W4A8_F32 and 16 with the
  * 16-bit types; everything is accumulated in fp32.  Infinities and NaN reach the outputs of

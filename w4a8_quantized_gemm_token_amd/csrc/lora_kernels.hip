@@ -285,65 +285,72 @@ __device__ __forceinline__ int sum_upto(int v) {
     return v + __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
 }
 
-// More tiles: the table by one workgroup, wave w the tiles w, w + 16, ...  Latency of its two passes over the ids: 313
-// tiles take 24 us, in a call of 530.
+// More tiles: the table by one workgroup, wave w the tiles w, w + 16, ..., all ids and first rows in LDS, from where the
+// entries are written once their places are known.  313 tiles take 20 us, in a call of 526 (24 us with 4 KB of LDS and the
+// ids read and compared twice); a wave's 20 tiles stand one after another.
 constexpr int kTableThreads = 1024, kTableWaves = kTableThreads / kWave, kMaxTiles = kSlab / kTile;
 __global__ __launch_bounds__(kTableThreads) void lora_table_kernel(const LoraArgs a, int64_t m0, int rows, int most) {
-    __shared__ __attribute__((aligned(16))) int ids[kTableWaves][kWave];
+    __shared__ __attribute__((aligned(16))) int ids[kMaxTiles][kWave];
+    __shared__ uint64_t leaders[kMaxTiles];
     __shared__ int counts[kMaxTiles], bare[kMaxTiles];
     const int lane = threadIdx.x % kWave, wave = wave_id(), tiles = tiles_in(rows);
-    for (int pass = 0; pass < 2; ++pass) {
-        for (int t0 = wave; t0 < tiles; t0 += 4 * kTableWaves) {
-            int id[4], tile[4], at[4], rest[4];  // four tiles under way together
+    constexpr int kTogether = 8;  // tiles whose ids are under way together
+    for (int t0 = wave; t0 < tiles; t0 += kTogether * kTableWaves) {
+        int id[kTogether];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                tile[i] = t0 + i * kTableWaves;
-                const int row = tile[i] * kTile + lane;
-                id[i] = row < rows ? a.row_adapter[m0 + row] : -1;
-                at[i] = tile[i] < tiles ? counts[tile[i]] : 0;
-                rest[i] = tile[i] < tiles ? bare[tile[i]] : 0;
-            }
-            const Tile t[4] = {Tile(id[0], a.L, ids[wave]), Tile(id[1], a.L, ids[wave]), Tile(id[2], a.L, ids[wave]),
-                               Tile(id[3], a.L, ids[wave])};
-            if (pass) {
-                write_groups<4>(a, t, rows, tile, at, rest);
-            } else {
+        for (int i = 0; i < kTogether; ++i) {
+            const int row = (t0 + i * kTableWaves) * kTile + lane;
+            id[i] = row < rows ? a.row_adapter[m0 + row] : -1;
+        }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint64_t in = __ballot(tile[i] * kTile + lane < rows);
-                    if (lane == 0 && tile[i] < tiles) {
-                        counts[tile[i]] = t[i].groups();
-                        bare[tile[i]] = a.base != a.out && in != t[i].valid ? 1 : 0;
-                    }
-                }
+        for (int i = 0; i < kTogether; ++i) {
+            const int tile = t0 + i * kTableWaves;
+            if (tile >= tiles) break;
+            const Tile t(id[i], a.L, ids[tile]);
+            const uint64_t in = __ballot(tile * kTile + lane < rows);
+            ids[tile][lane] = id[i];
+            if (lane == 0) {
+                counts[tile] = t.groups();
+                bare[tile] = a.base != a.out && in != t.valid ? 1 : 0;
+                leaders[tile] = t.leaders;
             }
         }
-        lds_barrier();
-        if (pass == 0) {
-            if (wave == 0) {
-                // counts become the numbers of first groups
-                constexpr int kMine = kMaxTiles / kWave;
-                int c = 0, b = 0;
-                for (int i = 0; i < kMine; ++i)
-                    if (lane * kMine + i < tiles) c += counts[lane * kMine + i], b += bare[lane * kMine + i];
-                const int cs = sum_upto(c), bs = sum_upto(b), groups = __builtin_amdgcn_readlane(cs, kWave - 1);
-                int at = cs - c, bat = groups + bs - b;
-                for (int i = 0; i < kMine; ++i)
-                    if (lane * kMine + i < tiles) {
-                        const int n = counts[lane * kMine + i], f = bare[lane * kMine + i];
-                        counts[lane * kMine + i] = at;
-                        bare[lane * kMine + i] = bat;
-                        at += n;
-                        bat += f;
-                    }
-                if (lane == kWave - 1) {
-                    Head h{groups, bs, 0, 0, {}};
-                    set_ranges(h, rows, a.K, a.R, most);
-                    *head_of(a) = h;
-                }
+    }
+    lds_barrier();
+    if (wave == 0) {
+        // counts become the numbers of first groups
+        constexpr int kMine = kMaxTiles / kWave;
+        int c = 0, b = 0;
+        for (int i = 0; i < kMine; ++i)
+            if (lane * kMine + i < tiles) c += counts[lane * kMine + i], b += bare[lane * kMine + i];
+        const int cs = sum_upto(c), bs = sum_upto(b), groups = __builtin_amdgcn_readlane(cs, kWave - 1);
+        int at = cs - c, bat = groups + bs - b;
+        for (int i = 0; i < kMine; ++i)
+            if (lane * kMine + i < tiles) {
+                const int n = counts[lane * kMine + i], f = bare[lane * kMine + i];
+                counts[lane * kMine + i] = at;
+                bare[lane * kMine + i] = bat;
+                at += n;
+                bat += f;
             }
-            lds_barrier();
+        if (lane == kWave - 1) {
+            Head h{groups, bs, 0, 0, {}};
+            set_ranges(h, rows, a.K, a.R, most);
+            *head_of(a) = h;
         }
+    }
+    lds_barrier();
+    for (int t0 = wave; t0 < tiles; t0 += 4 * kTableWaves) {
+        int tile[4], at[4], rest[4];
+        const auto entry = [&](int i) {
+            tile[i] = t0 + i * kTableWaves;
+            const bool in = tile[i] < tiles;
+            at[i] = in ? counts[tile[i]] : 0;
+            rest[i] = in ? bare[tile[i]] : 0;
+            return Tile(in ? ids[tile[i]][lane] : -1, a.L, in ? leaders[tile[i]] : 0);
+        };
+        const Tile t[4] = {entry(0), entry(1), entry(2), entry(3)};
+        write_groups<4>(a, t, rows, tile, at, rest);
     }
 }
 
