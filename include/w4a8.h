@@ -350,7 +350,7 @@ w4a8_status w4a8_lora_add(const void *x, int32_t x_type, int64_t ldx, int64_t M,
  * b NULL: 0).  Everything up to z is taken in fp64, so that codes do not turn on the order of
  * fp32 sums; each output is rounded to fp32 and from there to its type (values past a 16-bit
  * type's range become infinities).  The scale is a product, as tensor code on this device forms
- * max / 127, so that the codes are those of the unfused steps bit for bit; w4a8_quantize_act's
+ * max / 127, so that equal z give the scale and codes of the unfused steps bit for bit; w4a8_quantize_act's
  * quotient is within one fp32 step of it.  A row with s == 0 gets codes 0.
  *   res, y, gate, z_out: rows of res_type, y_type, gate_type, z_type with strides ldr, ldy,
  *   ldg, ldz; res_out of res_type, stride ldro.  The elements between rows are not written.
