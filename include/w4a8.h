@@ -321,9 +321,10 @@ w4a8_status w4a8_moe_grouped_gemm_w8a8(const int8_t *qa, const float *a_scale, i
  *   overlap.  No other input overlaps out or the workspace.  Entries of A and B past rank_a are not used, whatever they hold.
  * Equal calls give equal bytes; the order in which a row's sums are taken may turn on the call's other rows.
  * How exactly the two products take part: x and v enter the matrix cores as sums of 16-bit
- * values that together hold at least 22 bits of each with out_type W4A8_F32 and 16 with the
- * 16-bit types; everything is accumulated in fp32.  Infinities and NaN reach the outputs of
- * their own row (x) or column (B) or adapter (A) only; an infinity may become NaN on the way.
+ * values that together hold all bits of x, and all of v beside W4A8_BF16 weights; beside
+ * W4A8_F16 weights v_j is held to 2^-23 of itself or 2^-39 of its row's largest.  Everything is
+ * accumulated in fp32, whatever out_type.  Infinities and NaN reach the outputs of their own
+ * row (x) or column (B) or adapter (A) only; an infinity may become NaN on the way.
  * Any M >= 0 and N in [1, 2^23]; K a positive multiple of 8 up to 2^20; R a multiple of 8 in
  * [8, 256]; 1 <= L <= 65536; row strides below 2^24.  A, B and workspace 16-byte aligned, x, base and out aligned to
  * their element.  workspace: device memory of at least w4a8_lora_workspace_size(M, K, L, R)

@@ -8,10 +8,11 @@
 // twice.  The groups stand in a table in the workspace, which a workgroup of the shrink product writes, or a launch of
 // its own in front of it above 64 tiles.  Longer calls go by slabs of 32768 rows.
 //
-// Arithmetic: the matrix cores take 16-bit operands.  fp32 values enter as sums of bf16 parts, each
-// the next 8 bits cut off the rest (three hold all 24, two hold 16, which 16-bit outputs do with);
-// an fp16 value beside bf16 is two such parts, exactly.  v meets fp16 weights as two fp16 parts (22
-// bits) after a scaling of its row by a power of two.  All sums are fp32.
+// Arithmetic: the matrix cores take 16-bit operands.  fp32 values enter as sums of three bf16 parts, each the rest of the
+// ones before it rounded to its 8 bits, which hold all 24 bits whatever the output's type (rows may cancel, and then bits
+// that the output's rounding seems to hide are all that is left); an fp16 value beside bf16 is two such parts, exactly.  v
+// meets fp16 weights as two fp16 parts after a scaling of its row by a power of two: within 2^-23 of each entry, or 2^-39 of
+// the row's largest, below what its own fp32 sum leaves open.  All sums are fp32.
 //
 // What has to move: x, base and out once, and the A and B of the adapters in use.  Times and bounds stand at the kernels
 // for these calls (rows; adapters in use; rank; k; columns): one token (1; 1; 16; 7168; 4096), decode batch (64; 48; 16;
@@ -78,35 +79,33 @@ __device__ __forceinline__ int quotient(int a, int b, int &rest) {
 }
 
 // ------------------------------------------------------------------ operands in parts
-// part[i] = the next 8 bits of v, cut off; an infinity has no rest.
+// part[i] = what the parts before it leave of v, rounded to nearest: N parts hold 8 N bits and more.  All but the last stay
+// inside bf16's finite range: above it the rounding would give an infinity (and the rest another one of the other sign), and
+// an infinity or NaN has to reach one part only, the last, from where it meets the other operand's first part.
 template <int N>
 __device__ __forceinline__ void split(const float (&v)[8], bf8 (&part)[N]) {
+    constexpr float kTop = 0x1.FEp+127f;  // bf16's largest
     float r[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) r[e] = v[e];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        v4u o;
 #pragma unroll
-        for (int e = 0; e < 8; e += 2)
-            o[e / 2] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, r[e + 1]), __builtin_bit_cast(uint32_t, r[e]),
-                                             0x07060302);
-        part[i] = __builtin_bit_cast(bf8, o);
-        if (i + 1 < N) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float head = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, r[e]) & 0xFFFF0000u);
-                const float rest = r[e] - head;
-                r[e] = i == 0 && __builtin_amdgcn_classf(r[e], 0x204) ? 0.0f : rest;
+        for (int e = 0; e < 8; ++e) {
+            if (i + 1 == N) {
+                part[i][e] = (__bf16)r[e];
+            } else {
+                part[i][e] = (__bf16)__builtin_amdgcn_fmed3f(r[e], -kTop, kTop);
+                r[e] -= (float)part[i][e];
             }
         }
     }
 }
 
-// The operand of type T beside one of type U: itself where both are the same 16-bit type, parts otherwise (P for fp32).
-template <typename T, typename U, int P>
+// The operand of type T beside one of type U: itself where both are the same 16-bit type, parts otherwise (three for fp32).
+template <typename T, typename U>
 struct Operand {
-    static constexpr int kParts = std::is_same<T, float>::value ? P : std::is_same<T, _Float16>::value ? 2 : 1;
+    static constexpr int kParts = std::is_same<T, float>::value ? 3 : std::is_same<T, _Float16>::value ? 2 : 1;
     typedef bf8 V;
     static __device__ __forceinline__ void of(const Eight<T> &x, V (&part)[kParts]) {
         if constexpr (std::is_same<T, __bf16>::value) {
@@ -119,8 +118,8 @@ struct Operand {
         }
     }
 };
-template <int P>
-struct Operand<_Float16, _Float16, P> {
+template <>
+struct Operand<_Float16, _Float16> {
     static constexpr int kParts = 1;
     typedef h8 V;
     static __device__ __forceinline__ void of(const Eight<_Float16> &x, V (&part)[1]) { part[0] = x; }
@@ -361,11 +360,11 @@ constexpr int kRound = RT == 1 ? 4 : 8;
 
 // v[token][j] over windows [w0, w1) of k for cnt rows in list and 16 RT ranks from j0; waves take windows in turn.
 // Matrix rows are ranks, matrix columns tokens.
-template <typename X, typename W, int P, int TT, int RT>
+template <typename X, typename W, int TT, int RT>
 __device__ __forceinline__ void shrink_group(const LoraArgs &a, int64_t row0, int64_t slab, int id, int rank, int j0, int cnt,
                                              const uint8_t *list, int w0, int w1, float *part, f4 (*red)[kRound<RT>][kWave]) {
-    using OX = Operand<X, W, P>;
-    using OW = Operand<W, X, P>;
+    using OX = Operand<X, W>;
+    using OW = Operand<W, X>;
     const int wave = wave_id(), lane = threadIdx.x % kWave, col = lane % 16, g = lane / 16;
     const X *px = (const X *)a.x + row0 * a.ldx;
     const W *pw = (const W *)a.A + (int64_t)id * a.R * a.K;
@@ -397,8 +396,8 @@ __device__ __forceinline__ void shrink_group(const LoraArgs &a, int64_t row0, in
                     for (int p = 0; p < OX::kParts; ++p)
 #pragma unroll
                         for (int q = 0; q < OW::kParts; ++q)
-                            // products of parts that lie below what the parts hold are left out
-                            if (q == 0 || p + q < (OX::kParts > 1 ? OX::kParts : 2)) acc[t][r] = mfma(fw[r][q], fx[p], acc[t][r]);
+                            // (the third part of x beside the second of an fp16 weight: 2^-27 of the product)
+                            if (p + q < 3) acc[t][r] = mfma(fw[r][q], fx[p], acc[t][r]);
             }
         }
     };
@@ -456,7 +455,7 @@ __device__ __forceinline__ void shrink_group(const LoraArgs &a, int64_t row0, in
 // last round of units leaves CUs idle.  Units of 32 rows with twice the waves a CU spilled and were slower; grids of
 // 256 to 2048 take the same time.  SELF: every workgroup finds the groups for itself, and the last one writes the table
 // for the expand product.
-template <typename X, typename W, int P, int RT, bool SELF>
+template <typename X, typename W, int RT, bool SELF>
 __global__ __launch_bounds__(kShrinkThreads) void lora_shrink_kernel(const LoraArgs a, int64_t m0, int rows, int most) {
     __shared__ f4 red[kShrinkWaves][kRound<RT>][kWave];
     __shared__ __attribute__((aligned(16))) int ids[SELF ? kSelf : 1][kWave];  // of all tiles
@@ -532,18 +531,18 @@ __global__ __launch_bounds__(kShrinkThreads) void lora_shrink_kernel(const LoraA
         const int64_t slab = (int64_t)g.tile * kTile, row0 = m0 + slab;
         const int w0 = split * h.per, w1 = min(w0 + h.per, windows);
         float *part = parts_of(a, rows) + (int64_t)split * rows * a.R;
-        if (cnt <= 16) shrink_group<X, W, P, 1, RT>(a, row0, slab, g.adapter, g.rank, j0, cnt, list, w0, w1, part, red);
-        else if (cnt <= 32) shrink_group<X, W, P, 2, RT>(a, row0, slab, g.adapter, g.rank, j0, cnt, list, w0, w1, part, red);
-        else shrink_group<X, W, P, 4, RT>(a, row0, slab, g.adapter, g.rank, j0, cnt, list, w0, w1, part, red);
+        if (cnt <= 16) shrink_group<X, W, 1, RT>(a, row0, slab, g.adapter, g.rank, j0, cnt, list, w0, w1, part, red);
+        else if (cnt <= 32) shrink_group<X, W, 2, RT>(a, row0, slab, g.adapter, g.rank, j0, cnt, list, w0, w1, part, red);
+        else shrink_group<X, W, 4, RT>(a, row0, slab, g.adapter, g.rank, j0, cnt, list, w0, w1, part, red);
     }
 }
 
 // ------------------------------------------------------------------ expand
-// v beside weights of type W: bf16 parts as above (P of them), or two fp16 parts of the scaled row.
-template <typename W, int P>
+// v beside weights of type W: bf16 parts as above, or two fp16 parts of the scaled row.
+template <typename W>
 struct Held {
     static constexpr bool kScaled = std::is_same<W, _Float16>::value;
-    static constexpr int kParts = kScaled ? 2 : P;
+    static constexpr int kParts = kScaled ? 2 : 3;
 };
 
 // Entries from the n-th on become 0: ranks past the adapter's own, whatever they hold.
@@ -555,8 +554,8 @@ __device__ __forceinline__ void cut(Eight<W> &x, int n) {
 
 // Workgroups a CU: three, where the rows of v leave LDS for them.
 constexpr int kExpandBlocks = 3;
-template <typename W, int P, int KS>
-constexpr int kResident = KS > 4 ? 1 : KS == 4 && Held<W, P>::kParts == 3 ? 2 : kExpandBlocks;
+template <typename W, int KS>
+constexpr int kResident = KS > 4 ? 1 : KS == 4 && Held<W>::kParts == 3 ? 2 : kExpandBlocks;
 constexpr int kUnit = 128;  // columns that a workgroup's share of a group is counted in
 
 // Columns of a wave's step of NT matrix tiles, dealt so that a lane has 16 bytes of output columns in a row: piece p of the
@@ -574,11 +573,11 @@ struct Columns {
 };
 
 // Columns [n0, n1) of a group's rows; n0 is a multiple of kUnit, n1 too or N.  stage() puts the group's v into vp and undo.
-template <typename W, typename T, int P, int KS, int TT, typename Stage>
+template <typename W, typename T, int KS, int TT, typename Stage>
 __device__ __forceinline__ void expand_group(const LoraArgs &a, int64_t row0, int id, int rank, float scale, int cnt, const uint8_t *list,
                                              const Eight<W> *vp, const float *undo, int64_t n0, int64_t n1, Stage &&stage) {
     // the fewer rows and ranks, the more columns a step, for loads under way
-    constexpr int NT = TT * KS <= 2 ? 4 : 2, kParts = Held<W, P>::kParts;
+    constexpr int NT = TT * KS <= 2 ? 4 : 2, kParts = Held<W>::kParts;
     using C = Columns<T, NT>;
     const int wave = wave_id(), lane = threadIdx.x % kWave, col = lane % 16, g = lane / 16;
     const W *pb = (const W *)a.B + (int64_t)id * a.N * a.R;
@@ -619,7 +618,7 @@ __device__ __forceinline__ void expand_group(const LoraArgs &a, int64_t row0, in
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
         const int i = t * 16 + col;
-        f[t] = Held<W, P>::kScaled ? scale * undo[i < cnt ? i : 0] : scale;
+        f[t] = Held<W>::kScaled ? scale * undo[i < cnt ? i : 0] : scale;
     }
     for (; n < whole; n += kWaves * C::kStep) {
         if (rank & 7) {
@@ -674,7 +673,7 @@ __device__ __forceinline__ void expand_group(const LoraArgs &a, int64_t row0, in
 #pragma unroll
             for (int p = 0; p < kParts; ++p) acc = mfma(b[ks], vp[((p * KS + ks) * kTile + i) * 4 + g], acc);
         }
-        const float fi = Held<W, P>::kScaled ? scale * undo[i] : scale;
+        const float fi = Held<W>::kScaled ? scale * undo[i] : scale;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (i < cnt && c + 4 * g + e < n1) out[row * a.ldo + c + 4 * g + e] = (T)((float)old[e] + fi * acc[e]);
@@ -684,15 +683,15 @@ __device__ __forceinline__ void expand_group(const LoraArgs &a, int64_t row0, in
 // The rows of v of a group in LDS, as the matrix instruction's columns: vp[part][ks][token][g], 8 ranks each.  Where the
 // group has fewer eights of ranks than there are threads, the ranges of k are shared out over threads too and meet in
 // `some`, so that few rows wait for one or two loads and not for one after another.
-template <typename W, int P, int KS>
+template <typename W, int KS>
 __device__ __forceinline__ void stage_v(const LoraArgs &a, int64_t slab, int rank, int cnt, const uint8_t *list, int rows,
                                         int splits, Eight<W> *vp, float *undo, uint32_t *top, Eight<float> *some) {
-    constexpr int kParts = Held<W, P>::kParts;
+    constexpr int kParts = Held<W>::kParts;
     const int t = threadIdx.x, tokens = (cnt + 15) / 16 * 16, eights = (rank + 7) / 8;
     constexpr int all = KS * 4;  // eights of a token, those past the rank 0
     const float *parts = parts_of(a, rows) + slab * a.R;
     const int64_t range = (int64_t)rows * a.R;
-    if constexpr (Held<W, P>::kScaled) {
+    if constexpr (Held<W>::kScaled) {
         if (t < kTile) top[t] = 0;
         lds_barrier();
     }
@@ -702,7 +701,7 @@ __device__ __forceinline__ void stage_v(const LoraArgs &a, int64_t slab, int ran
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = i < cnt && j * 8 + e < rank ? sum[e] : 0.0f;
-        if constexpr (Held<W, P>::kScaled) {
+        if constexpr (Held<W>::kScaled) {
             float m = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) m = __builtin_isfinite(v[e]) ? fmaxf(m, fabsf(v[e])) : m;
@@ -746,7 +745,7 @@ __device__ __forceinline__ void stage_v(const LoraArgs &a, int64_t slab, int ran
 #pragma unroll 1
         for (int u = t; u < entries; u += kThreads) put(u, add(u, 0, 1));
     }
-    if constexpr (Held<W, P>::kScaled) {
+    if constexpr (Held<W>::kScaled) {
         // the largest finite entry of each row goes to [2^14, 2^15): two fp16 parts then hold 22 bits of it, and
         // of smaller entries all that lies above 2^-38 of it
         lds_barrier();
@@ -797,10 +796,10 @@ __device__ __forceinline__ void copy_rows(const LoraArgs &a, int64_t row0, int c
 // loop, staging 64 rows of 128 ranks in front of each run, and groups of large and of small rank side by side.
 // Decode batch 18 us and one token 6 us are latency: the table, the parts of v, and a run of steps whose loads (base and
 // B) are one step ahead.
-template <typename W, typename T, int P, int KS>
-__global__ __launch_bounds__(kThreads, (kResident<W, P, KS>)) void lora_expand_kernel(const LoraArgs a, int64_t m0,
+template <typename W, typename T, int KS>
+__global__ __launch_bounds__(kThreads, (kResident<W, KS>)) void lora_expand_kernel(const LoraArgs a, int64_t m0,
                                                                                                 int rows, int most) {
-    __shared__ Eight<W> vp[Held<W, P>::kParts * KS * kTile * 4];
+    __shared__ Eight<W> vp[Held<W>::kParts * KS * kTile * 4];
     __shared__ float undo[kTile];
     __shared__ uint32_t top[kTile];
     __shared__ Eight<float> some[kThreads];
@@ -844,10 +843,10 @@ __global__ __launch_bounds__(kThreads, (kResident<W, P, KS>)) void lora_expand_k
             copy_rows<T>(a, row0, cnt, list, n0, n1);
             continue;
         }
-        const auto stage = [&] { stage_v<W, P, KS>(a, slab, rank, cnt, list, rows, splits, vp, undo, top, some); };
-        if (cnt <= 16) expand_group<W, T, P, KS, 1>(a, row0, ad, rank, g.scale, cnt, list, vp, undo, n0, n1, stage);
-        else if (cnt <= 32) expand_group<W, T, P, KS, 2>(a, row0, ad, rank, g.scale, cnt, list, vp, undo, n0, n1, stage);
-        else expand_group<W, T, P, KS, 4>(a, row0, ad, rank, g.scale, cnt, list, vp, undo, n0, n1, stage);
+        const auto stage = [&] { stage_v<W, KS>(a, slab, rank, cnt, list, rows, splits, vp, undo, top, some); };
+        if (cnt <= 16) expand_group<W, T, KS, 1>(a, row0, ad, rank, g.scale, cnt, list, vp, undo, n0, n1, stage);
+        else if (cnt <= 32) expand_group<W, T, KS, 2>(a, row0, ad, rank, g.scale, cnt, list, vp, undo, n0, n1, stage);
+        else expand_group<W, T, KS, 4>(a, row0, ad, rank, g.scale, cnt, list, vp, undo, n0, n1, stage);
     }
 }
 
@@ -858,22 +857,22 @@ int most_splits(int64_t rows, int64_t K) {
     return (int)std::max<int64_t>(1, std::min(std::max<int64_t>(4, kTarget / tiles), windows / kShrinkWaves));
 }
 
-template <typename X, typename W, int P>
+template <typename X, typename W>
 void shrink(const LoraArgs &a, int64_t m0, int rows, hipStream_t stream) {
     const int rt = a.R <= 16 ? 1 : a.R <= 32 ? 2 : 4, most = most_splits(rows, a.K);
     const int64_t tiles = (rows + kTile - 1) / kTile;
     const int64_t units = tiles * std::min<int64_t>({kTile, rows, a.L}) * blocks_of(a.R) * most;
     const uint32_t grid = (uint32_t)std::min<int64_t>(units, kTarget);
 #define W4A8_SHRINK(RT)                                                                                            \
-    (tiles > kSelf ? lora_shrink_kernel<X, W, P, RT, false><<<grid, kShrinkThreads, 0, stream>>>(a, m0, rows, most) \
-                   : lora_shrink_kernel<X, W, P, RT, true><<<grid, kShrinkThreads, 0, stream>>>(a, m0, rows, most))
+    (tiles > kSelf ? lora_shrink_kernel<X, W, RT, false><<<grid, kShrinkThreads, 0, stream>>>(a, m0, rows, most) \
+                   : lora_shrink_kernel<X, W, RT, true><<<grid, kShrinkThreads, 0, stream>>>(a, m0, rows, most))
     if (rt == 1) W4A8_SHRINK(1);
     else if (rt == 2) W4A8_SHRINK(2);
     else W4A8_SHRINK(4);
 #undef W4A8_SHRINK
 }
 
-template <typename W, typename T, int P>
+template <typename W, typename T>
 void expand(const LoraArgs &a, int64_t m0, int rows, hipStream_t stream) {
     const int64_t tiles = (rows + kTile - 1) / kTile;
     // no more workgroups than there can be units; as many as are resident, or where those would have long runs each, more
@@ -881,7 +880,7 @@ void expand(const LoraArgs &a, int64_t m0, int rows, hipStream_t stream) {
     const int64_t units = tiles * std::min<int64_t>({kTile, rows, (int64_t)a.L + 1}) * ((a.N + kUnit - 1) / kUnit);
     const int64_t runs = tiles * ((a.N + kUnit - 1) / kUnit) / 12;
     const uint32_t grid = (uint32_t)std::min<int64_t>(units, std::max<int64_t>(256 * kExpandBlocks, std::min<int64_t>(runs, 1 << 20)));
-#define W4A8_EXPAND(KS) lora_expand_kernel<W, T, P, KS><<<grid, kThreads, 0, stream>>>(a, m0, rows, most_splits(rows, a.K))
+#define W4A8_EXPAND(KS) lora_expand_kernel<W, T, KS><<<grid, kThreads, 0, stream>>>(a, m0, rows, most_splits(rows, a.K))
     if (a.R <= 32) W4A8_EXPAND(1);
     else if (a.R <= 64) W4A8_EXPAND(2);
     else if (a.R <= 128) W4A8_EXPAND(4);
@@ -889,18 +888,18 @@ void expand(const LoraArgs &a, int64_t m0, int rows, hipStream_t stream) {
 #undef W4A8_EXPAND
 }
 
-template <typename W, int P>
+template <typename W>
 hipError_t launch_w(const LoraArgs &a, hipStream_t stream) {
     for (int64_t m0 = 0; m0 < a.M; m0 += kSlab) {
         const int rows = (int)std::min(a.M - m0, kSlab);
         if (tiles_in(rows) > kSelf)
             lora_table_kernel<<<1, kTableThreads, 0, stream>>>(a, m0, rows, most_splits(rows, a.K));
-        if (a.x_type == W4A8_F32) shrink<float, W, P>(a, m0, rows, stream);
-        else if (a.x_type == W4A8_F16) shrink<_Float16, W, 2>(a, m0, rows, stream);
-        else shrink<__bf16, W, 2>(a, m0, rows, stream);
-        if (a.out_type == W4A8_F32) expand<W, float, 3>(a, m0, rows, stream);
-        else if (a.out_type == W4A8_F16) expand<W, _Float16, 2>(a, m0, rows, stream);
-        else expand<W, __bf16, 2>(a, m0, rows, stream);
+        if (a.x_type == W4A8_F32) shrink<float, W>(a, m0, rows, stream);
+        else if (a.x_type == W4A8_F16) shrink<_Float16, W>(a, m0, rows, stream);
+        else shrink<__bf16, W>(a, m0, rows, stream);
+        if (a.out_type == W4A8_F32) expand<W, float>(a, m0, rows, stream);
+        else if (a.out_type == W4A8_F16) expand<W, _Float16>(a, m0, rows, stream);
+        else expand<W, __bf16>(a, m0, rows, stream);
         if (hipError_t err = hipGetLastError(); err != hipSuccess) return err;
     }
     return hipSuccess;
@@ -919,10 +918,7 @@ int64_t lora_ws_bytes(int64_t M, int64_t K, int32_t, int32_t R) {
 }
 
 hipError_t launch_lora_add(const LoraArgs &a, hipStream_t stream) {
-    // an fp32 output is held by three parts of fp32 operands, a 16-bit one by two
-    const bool wide = a.out_type == W4A8_F32;
-    if (a.ab_type == W4A8_F16) return wide ? launch_w<_Float16, 3>(a, stream) : launch_w<_Float16, 2>(a, stream);
-    return wide ? launch_w<__bf16, 3>(a, stream) : launch_w<__bf16, 2>(a, stream);
+    return a.ab_type == W4A8_F16 ? launch_w<_Float16>(a, stream) : launch_w<__bf16>(a, stream);
 }
 
 }  // namespace w4a8
