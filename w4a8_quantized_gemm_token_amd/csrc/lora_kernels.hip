@@ -584,7 +584,7 @@ __device__ __forceinline__ void expand_group(const LoraArgs &a, int64_t row0, in
     const T *base = (const T *)a.base + row0 * a.ldb;
     T *out = (T *)a.out + row0 * a.ldo;
     uint32_t ob[TT], oo[TT], ow[NT];  // bytes: 64 rows of strides below 2^24, 128 columns of 256 ranks
-    float f[TT];
+    float back[TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
         const int i = t * 16 + col;
@@ -594,6 +594,9 @@ __device__ __forceinline__ void expand_group(const LoraArgs &a, int64_t row0, in
     }
 #pragma unroll
     for (int q = 0; q < NT; ++q) ow[q] = (C::of(q, col) * a.R + 8 * g) * (uint32_t)sizeof(W);
+    // the row's power of two is taken back before the adapter's scale comes in: their product may leave fp32's range, or its
+    // normal numbers, where the term is an ordinary one
+    const auto term = [](float sum, float back) { return Held<W>::kScaled ? sum * back : sum; };
     typename C::V have[TT][C::kPieces];
     Eight<W> fb[KS][NT];
     const auto load = [&](int64_t n) {
@@ -618,7 +621,7 @@ __device__ __forceinline__ void expand_group(const LoraArgs &a, int64_t row0, in
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
         const int i = t * 16 + col;
-        f[t] = Held<W>::kScaled ? scale * undo[i < cnt ? i : 0] : scale;
+        back[t] = Held<W>::kScaled ? undo[i < cnt ? i : 0] : 1.0f;
     }
     for (; n < whole; n += kWaves * C::kStep) {
         if (rank & 7) {
@@ -648,7 +651,7 @@ __device__ __forceinline__ void expand_group(const LoraArgs &a, int64_t row0, in
                     typename C::V o;
 #pragma unroll
                     for (int i = 0; i < C::VW; ++i)
-                        o[i] = (T)((float)have[t][p][i] + f[t] * acc[t][(p * C::VW + i) / 4][i % 4]);
+                        o[i] = (T)((float)have[t][p][i] + scale * term(acc[t][(p * C::VW + i) / 4][i % 4], back[t]));
                     at<typename C::VU>(out + n + 4 * C::VW * p, oo[t]) = o;
                 }
             }
@@ -673,10 +676,10 @@ __device__ __forceinline__ void expand_group(const LoraArgs &a, int64_t row0, in
 #pragma unroll
             for (int p = 0; p < kParts; ++p) acc = mfma(b[ks], vp[((p * KS + ks) * kTile + i) * 4 + g], acc);
         }
-        const float fi = Held<W>::kScaled ? scale * undo[i] : scale;
+        const float one = Held<W>::kScaled ? undo[i] : 1.0f;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (i < cnt && c + 4 * g + e < n1) out[row * a.ldo + c + 4 * g + e] = (T)((float)old[e] + fi * acc[e]);
+            if (i < cnt && c + 4 * g + e < n1) out[row * a.ldo + c + 4 * g + e] = (T)((float)old[e] + scale * term(acc[e], one));
     }
 }
 
