@@ -328,7 +328,8 @@ w4a8_status w4a8_moe_grouped_gemm_w8a8(const int8_t *qa, const float *a_scale, i
  * Any M >= 0 and N in [1, 2^23]; K a positive multiple of 8 up to 2^20; R a multiple of 8 in
  * [8, 256]; 1 <= L <= 65536; row strides below 2^24.  A, B and workspace 16-byte aligned, x, base and out aligned to
  * their element.  workspace: device memory of at least w4a8_lora_workspace_size(M, K, L, R)
- * bytes; its contents need not be set or kept, and calls that may overlap (other streams,
+ * bytes, which never falls as M, K, L or R grows: one of the largest sizes serves every smaller
+ * call.  Its contents need not be set or kept, and calls that may overlap (other streams,
  * graphs replayed side by side) need one each.
  * Errors: W4A8_EINVAL (null, bad sizes, strides or alignment), W4A8_EUNSUPPORTED (another
  * type), W4A8_EWORKSPACE.  M == 0 is a no-op. */

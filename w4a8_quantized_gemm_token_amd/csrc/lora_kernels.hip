@@ -912,12 +912,14 @@ hipError_t launch_w(const LoraArgs &a, hipStream_t stream) {
 
 namespace w4a8 {
 
+// Room for the first slab, which is the largest.  The parts of v of `rows` rows are most_splits(rows) * rows * R, and that falls
+// here and there as rows grow, so that a smaller batch can have more of them; the room is for the least bound that does not:
+// rows * kTarget / tiles <= kTile * kTarget, and 4 * rows (most_splits' two terms), of as many ranges as there are windows for.
 int64_t lora_ws_bytes(int64_t M, int64_t K, int32_t, int32_t R) {
     if (M == 0) return 0;
-    // the first slab is the largest, a last and shorter one may have more ranges of k
-    const auto need = [&](int64_t rows) { return parts_at((int)rows) + most_splits(rows, K) * rows * R * 4; };
-    const int64_t first = std::min(M, kSlab), last = M % kSlab;
-    return std::max(need(first), last ? need(last) : 0);
+    const int64_t rows = std::min(M, kSlab), windows = (K + kWindow - 1) / kWindow;
+    const int64_t held = std::min(std::max<int64_t>(1, windows / kShrinkWaves) * rows, std::max<int64_t>(kTile * kTarget, 4 * rows));
+    return parts_at((int)rows) + held * R * 4;
 }
 
 hipError_t launch_lora_add(const LoraArgs &a, hipStream_t stream) {
