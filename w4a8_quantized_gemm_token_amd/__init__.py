@@ -458,6 +458,7 @@ def _lora_args(out, x, row_adapter, A, B, workspace, scale, ranks, base):
     L, R = A.shape[0], A.shape[1]
     N = B.shape[1]
     base = out if base is None else base
+    assert workspace is not None, "workspace: uint8 [lora_workspace(M, K, L, R)] expected"
     _is(A, (L, R, K), A.dtype, "A")
     _is(B, (L, N, R), A.dtype, "B")
     _is(row_adapter, (M,), torch.int32, "row_adapter")
