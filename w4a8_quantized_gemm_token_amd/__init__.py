@@ -501,6 +501,7 @@ def _norm_args(res, y, outs, post, post_w, post_b, gate, res_scale, y_scale, pre
     torch = _torch()
     res_out, z, qa, a_scale = outs
     like = res if res is not None else y
+    assert like is not None, "res or y expected"
     M, H = like.shape
     assert post in NORMS and pre in NORMS, f"norm: one of {sorted(NORMS)} expected"
     stream_type = res.dtype if res is not None else res_out.dtype if res_out is not None else torch.float32
@@ -537,6 +538,7 @@ def residual_norm_quantize(res, y=None, post: str = "none", post_w=None, post_b=
     Returns (stream, z or None, qa or None, a_scale or None); z is written if z_dtype is given."""
     torch = _torch()
     like = res if res is not None else y
+    assert like is not None, "res or y expected"
     M, H = like.shape
     if res_out is None:
         res_out = _empty((M, H), like.dtype, like)
