@@ -363,8 +363,8 @@ w4a8_status w4a8_lora_add(const void *x, int32_t x_type, int64_t ldx, int64_t M,
  *   An output may be an input itself (the same pointer, type and stride: the stream updated in
  *   place); otherwise outputs overlap nothing.
  * Any M >= 0, 1 <= H <= 32768.  res, y, gate, res_out and z_out aligned to their element, qa
- * 16-byte aligned.  eps at least 1e-40, the scales finite.  A row whose z is not finite gets
- * unspecified codes, as in w4a8_quantize_act; other rows are not affected.
+ * 16-byte aligned.  eps at least 1e-40, the scales within fp32's range.  A row whose z is not
+ * finite gets unspecified codes, as in w4a8_quantize_act; other rows are not affected.
  * Errors: W4A8_EINVAL (null, bad sizes, strides, alignment or values), W4A8_EUNSUPPORTED
  * (another type or norm).  M == 0 is a no-op. */
 #define W4A8_NORM_NONE 0

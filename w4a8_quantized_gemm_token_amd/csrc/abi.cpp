@@ -12,6 +12,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <limits>
 #include <thread>
 #include <vector>
 
@@ -581,8 +582,10 @@ w4a8_status w4a8_residual_norm_quantize(const void *res, int32_t res_type, int64
                      (((uintptr_t)post_w | (uintptr_t)post_b | (uintptr_t)pre_w | (uintptr_t)pre_b |
                        (uintptr_t)a_scale) & 3u) == 0,
                  W4A8_EINVAL, "qa must be 16-byte aligned, the others aligned to their elements");
-    W4A8_REQUIRE(std::isfinite(eps) && eps >= 1e-40 && std::isfinite(res_scale) && std::isfinite(y_scale), W4A8_EINVAL,
-                 "eps must be at least 1e-40, the scales finite");
+    // (within fp32's range no product of an input, weight, gate, 1 / sqrt(eps) and scale leaves fp64's)
+    const auto fp32 = [](double s) { return std::abs(s) <= (double)std::numeric_limits<float>::max(); };
+    W4A8_REQUIRE(std::isfinite(eps) && eps >= 1e-40 && fp32(res_scale) && fp32(y_scale), W4A8_EINVAL,
+                 "eps must be at least 1e-40, the scales within fp32's range");
     // an output that is an input has its layout, so that every element is read by the thread that writes it
     const auto same = [&](const void *o, int32_t ot, int64_t lo, const void *i, int32_t it, int64_t li) {
         return !o || o != i || (ot == it && (M == 1 || lo == li));
