@@ -311,8 +311,8 @@ w4a8_status w4a8_moe_grouped_gemm_w8a8(const int8_t *qa, const float *a_scale, i
  *     v_j       = sum_k x[m][k] * A[a][j][k]                          j < rank_a
  *     out[m][n] = T(base[m][n] + scale[a] * sum_j v_j * B[a][n][j])   T by out_type
  * in fp32 with one rounding to T; a row whose a is outside [0, L) has no adapter, and
- * out[m] = base[m].  Rows may come in any order of adapters; rows of one adapter that stand
- * within 64 rows of each other share its weights' loads.
+ * out[m] = base[m].  Rows may come in any order of adapters; rows of one adapter that stand in
+ * the same 64 rows of the call (64 i to 64 i + 63) share its weights' loads.
  *   x [M][K] of x_type (row stride ldx elements), A [L][R][K] and B [L][N][R] of ab_type
  *   (W4A8_F16 or W4A8_BF16), row_adapter int32 [M], ranks int32 [L] or NULL, scale fp32 [L]
  *   or NULL (1), base and out [M][N] of out_type (row strides ldb, ldo; the elements between
