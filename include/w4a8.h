@@ -325,9 +325,9 @@ w4a8_status w4a8_moe_grouped_gemm_w8a8(const int8_t *qa, const float *a_scale, i
  * W4A8_F16 weights v_j is held to 2^-23 of itself or 2^-39 of its row's largest.  Everything is
  * accumulated in fp32, whatever out_type.  Infinities and NaN reach the outputs of their own
  * row (x) or column (B) or adapter (A) only; an infinity may become NaN on the way.
- * Any M >= 0 and N in [1, 2^23]; K a positive multiple of 8 up to 2^20; R a multiple of 8 in
- * [8, 256]; 1 <= L <= 65536; row strides below 2^24.  A, B and workspace 16-byte aligned, x, base and out aligned to
- * their element.  workspace: device memory of at least w4a8_lora_workspace_size(M, K, L, R)
+ * 0 <= M < 2^31 and N in [1, 2^23]; K a positive multiple of 8 up to 2^20; R a multiple of 8 in
+ * [8, 256]; 1 <= L <= 65536; row strides below 2^24.  A, B and workspace 16-byte aligned, x, base
+ * and out aligned to their element.  workspace: device memory of at least w4a8_lora_workspace_size(M, K, L, R)
  * bytes, which never falls as M, K, L or R grows: one of the largest sizes serves every smaller
  * call.  Its contents need not be set or kept, and calls that may overlap (other streams,
  * graphs replayed side by side) need one each.
@@ -362,7 +362,7 @@ w4a8_status w4a8_lora_add(const void *x, int32_t x_type, int64_t ldx, int64_t M,
  *   fp32 [H] or NULL.
  *   An output may be an input itself (the same pointer, type and stride: the stream updated in
  *   place); otherwise outputs overlap nothing.
- * Any M >= 0, 1 <= H <= 32768.  res, y, gate, res_out and z_out aligned to their element, qa
+ * 0 <= M < 2^31, 1 <= H <= 32768.  res, y, gate, res_out and z_out aligned to their element, qa
  * 16-byte aligned.  eps at least 1e-40, the scales within fp32's range.  A row whose z is not
  * finite gets unspecified codes, as in w4a8_quantize_act; other rows are not affected.
  * Errors: W4A8_EINVAL (null, bad sizes, strides, alignment or values), W4A8_EUNSUPPORTED
