@@ -318,12 +318,15 @@ w4a8_status w4a8_moe_grouped_gemm_w8a8(const int8_t *qa, const float *a_scale, i
  *   or NULL (1), base and out [M][N] of out_type (row strides ldb, ldo; the elements between
  *   rows are not written).  base may be out itself (the same pointer and stride: the term is
  *   added in place and rows without an adapter are not touched); otherwise the two do not
- *   overlap.  No other input overlaps out or the workspace.  Entries of A and B past rank_a are not used, whatever they hold.
- * Equal calls give equal bytes; the order in which a row's sums are taken may turn on the call's other rows.
+ *   overlap.  No other input overlaps out or the workspace.  Entries of A and B past rank_a are
+ *   not used, whatever they hold.
+ * Equal calls give equal bytes; the order in which a row's sums are taken may turn on the call's
+ * other rows.
  * How exactly the two products take part: x and v enter the matrix cores as sums of 16-bit
- * values that together hold all bits of x, and all of v beside W4A8_BF16 weights; beside
- * W4A8_F16 weights v_j is held to 2^-23 of itself or 2^-39 of its row's largest.  Everything is
- * accumulated in fp32, whatever out_type.  Infinities and NaN reach the outputs of their own
+ * values that together hold all bits of x, and all of v beside W4A8_BF16 weights (those above
+ * 2^-134, half of bf16's least number); beside W4A8_F16 weights v_j is held to 2^-23 of itself
+ * or 2^-39 of its row's largest.  Everything is accumulated in fp32, whatever out_type.
+ * Infinities and NaN reach the outputs of their own
  * row (x) or column (B) or adapter (A) only; an infinity may become NaN on the way.
  * 0 <= M < 2^31 and N in [1, 2^23]; K a positive multiple of 8 up to 2^20; R a multiple of 8 in
  * [8, 256]; 1 <= L <= 65536; row strides below 2^24.  A, B and workspace 16-byte aligned, x, base
@@ -352,8 +355,9 @@ w4a8_status w4a8_lora_add(const void *x, int32_t x_type, int64_t ldx, int64_t M,
  * b NULL: 0).  Everything up to z is taken in fp64, so that codes do not turn on the order of
  * fp32 sums; each output is rounded to fp32 and from there to its type (values past a 16-bit
  * type's range become infinities).  The scale is a product, as tensor code on this device forms
- * max / 127, so that equal z give the scale and codes of the unfused steps bit for bit; w4a8_quantize_act's
- * quotient is within one fp32 step of it.  A row with s == 0 gets codes 0.
+ * max / 127, so that equal z give the scale and codes of the unfused steps bit for bit;
+ * w4a8_quantize_act's quotient is within one fp32 step of it, and its codes differ at most where
+ * z / s lies next to the middle of two.  A row with s == 0 gets codes 0.
  *   res, y, gate, z_out: rows of res_type, y_type, gate_type, z_type with strides ldr, ldy,
  *   ldg, ldz; res_out of res_type, stride ldro.  The elements between rows are not written.
  *   res NULL: 0.  y NULL: no block before (r' = S(res_scale * res); post is then NONE and gate
