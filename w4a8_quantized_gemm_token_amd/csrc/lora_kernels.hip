@@ -552,10 +552,14 @@ __device__ __forceinline__ void cut(Eight<W> &x, int n) {
     for (int e = 0; e < 8; ++e) x[e] = e < n ? x[e] : (W)0.0f;
 }
 
-// Workgroups a CU: three, where the rows of v leave LDS for them.
+// Workgroups a CU: three, one of ranks above 128.  Threads that share out the ranges of k in staging: all, but half of them
+// beside bf16 weights of 65 to 128 ranks, whose three parts leave LDS for three workgroups only then (500 rows of rank 128, k
+// 4096, 8192 columns: 30.1 us, with all threads and two workgroups 37.9; 8000 rows 148 against 167; one row the same).
 constexpr int kExpandBlocks = 3;
+template <int KS>
+constexpr int kResident = KS > 4 ? 1 : kExpandBlocks;
 template <typename W, int KS>
-constexpr int kResident = KS > 4 ? 1 : KS == 4 && Held<W>::kParts == 3 ? 2 : kExpandBlocks;
+constexpr int kSharing = KS == 4 && Held<W>::kParts == 3 ? kThreads / 2 : kThreads;
 constexpr int kUnit = 128;  // columns that a workgroup's share of a group is counted in
 
 // Columns of a wave's step of NT matrix tiles, dealt so that a lane has 16 bytes of output columns in a row: piece p of the
@@ -731,7 +735,7 @@ __device__ __forceinline__ void stage_v(const LoraArgs &a, int64_t slab, int ran
     };
     const int entries = tokens * all, bits = 32 - __builtin_clz(cnt * all - 1), wide = 1 << bits;  // cnt * all and more
     int share = 1;
-    while (share < splits && 2 * share * wide <= kThreads) share *= 2;
+    while (share < splits && 2 * share * wide <= kSharing<W, KS>) share *= 2;
     if (share > 1) {
         if (t < share * wide) some[t] = add(t % wide, t >> bits, share);
         lds_barrier();
@@ -800,12 +804,12 @@ __device__ __forceinline__ void copy_rows(const LoraArgs &a, int64_t row0, int c
 // Decode batch 18 us and one token 6 us are latency: the table, the parts of v, and a run of steps whose loads (base and
 // B) are one step ahead.
 template <typename W, typename T, int KS>
-__global__ __launch_bounds__(kThreads, (kResident<W, KS>)) void lora_expand_kernel(const LoraArgs a, int64_t m0,
+__global__ __launch_bounds__(kThreads, (kResident<KS>)) void lora_expand_kernel(const LoraArgs a, int64_t m0,
                                                                                                 int rows, int most) {
     __shared__ Eight<W> vp[Held<W>::kParts * KS * kTile * 4];
     __shared__ float undo[kTile];
     __shared__ uint32_t top[kTile];
-    __shared__ Eight<float> some[kThreads];
+    __shared__ Eight<float> some[kSharing<W, KS>];
     __shared__ uint8_t list[kTile];
     const Head *h = head_of(a);
     // (cut to what the workspace holds, as the table's entries are)
