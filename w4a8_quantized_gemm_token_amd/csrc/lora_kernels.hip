@@ -255,10 +255,10 @@ __device__ __forceinline__ void write_groups(const LoraArgs &a, const Tile (&t)[
 }
 
 // Ranges of k, and windows of each.  At least as many as make kFill units (group, block of ranks, range): 978 rows of one
-// adapter of rank 120 with k 5160 take 30 us, 50 without; with 256 units instead 34, and 1656 rows in 156 units 42 instead
-// of 34.  Beyond that up to kTarget units, or four ranges where there are as many units already (so that the last round
+// adapter of rank 120 with k 5160 and 4096 columns take 37 us, 46 without, and 1656 such rows 46 and 53; with 256 units 37
+// and 57.  Beyond that up to kTarget units, or four ranges where there are as many units already (so that the last round
 // of workgroups is a short one), if the expand product has not to read more than kStaged bytes of parts of v for a group on
-// average: with twice that the long prefill takes 570 us instead of 529, with half of it the prompts 32.0 instead of 31.3.
+// average: with twice that the long prefill takes 564 us instead of 520, with half of it 517, the prompts the same.
 // Never more than the workspace has room for.
 constexpr int kTarget = 512, kFill = 128, kStaged = 65536;
 constexpr int blocks_of(int R) { return R <= 64 ? 1 : (R + 63) / 64; }  // of ranks in the shrink product
@@ -285,7 +285,7 @@ __device__ __forceinline__ int sum_upto(int v) {
 }
 
 // More tiles: the table by one workgroup, wave w the tiles w, w + 16, ..., all ids and first rows in LDS, from where the
-// entries are written once their places are known.  313 tiles take 20 us, in a call of 526 (24 us with 4 KB of LDS and the
+// entries are written once their places are known.  313 tiles take 20 us, in a call of 520 (24 us with 4 KB of LDS and the
 // ids read and compared twice); a wave's 20 tiles stand one after another.
 constexpr int kTableThreads = 1024, kTableWaves = kTableThreads / kWave, kMaxTiles = kSlab / kTile;
 __global__ __launch_bounds__(kTableThreads) void lora_table_kernel(const LoraArgs a, int64_t m0, int rows, int most) {
@@ -448,11 +448,11 @@ __device__ __forceinline__ void shrink_group(const LoraArgs &a, int64_t row0, in
 }
 
 // A fixed grid walks units (group, block of ranks, range of k): 16 to 64 ranks (RT matrix tiles) against 16, 32 or 64
-// of the group's rows, eight waves sharing out the range.  One token 4.9 us and decode batch 6.9 us: finding the groups,
-// one or two windows' loads and adding the waves' sums up, one after another.  Prefill 23.6 us, 2.8 TB/s.  Long prefill
-// 178 us: 1.8 TB/s of x, where a window's loads, the cutting of its fp32 values into parts and its products (fp16
-// weights: two parts each) stand one after another in a wave, the other waves of a CU cover only part of that, and the
-// last round of units leaves CUs idle.  Units of 32 rows with twice the waves a CU spilled and were slower; grids of
+// of the group's rows, eight waves sharing out the range.  One token 5.0 us and decode batch 7.0 us: finding the groups,
+// one or two windows' loads and adding the waves' sums up, one after another.  Prefill 23.6 us, 2.8 TB/s.  Prompts 12 us.
+// Long prefill 178 us: 1.8 TB/s of x, where a window's loads, the making of parts of its fp32 values and of its fp16
+// weights (again for each 64 rows) and the products of parts stand one after another in a wave, the other waves of a CU
+// cover only part of that, and the last round of units leaves CUs idle.  Units of 32 rows with twice the waves a CU spilled and were slower; grids of
 // 256 to 2048 take the same time.  SELF: every workgroup finds the groups for itself, and the last one writes the table
 // for the expand product.
 template <typename X, typename W, int RT, bool SELF>
@@ -799,10 +799,12 @@ __device__ __forceinline__ void copy_rows(const LoraArgs &a, int64_t row0, int c
 
 // A fixed grid walks units (group, kUnit columns) in runs, columns fastest, so that a workgroup stages a group's v once
 // for all its columns, and tiles of few and of many groups cost what their work costs.  Prefill 62 us, 4.4 TB/s of base and
-// output, 5.6 TB/s once all workgroups are past their staging; long prefill 338 us, which is 3.4 TB/s: about 5 TB/s in the
-// loop, staging 64 rows of 128 ranks in front of each run, and groups of large and of small rank side by side.
-// Decode batch 18 us and one token 6 us are latency: the table, the parts of v, and a run of steps whose loads (base and
-// B) are one step ahead.
+// output.  Long prefill 338 us, which is 3.4 TB/s: each of some nine workgroups a group adds up and parts the same 64 rows of
+// 128 ranks in front of its run.  Prompts 22 us: the same by some 54 workgroups a group.  Decode batch 18 us (3.2 TB/s) and one
+// token 6 us are latency: the table, the parts of v, then steps whose loads (base and B) stand behind the last step's stores
+// and right in front of the products that need them, so that only the CU's other waves, eleven at most, cover them.  Ranks
+// above 128 leave one workgroup a CU: 4096 rows of rank 256, k 4096, 8192 columns 186 us with fp16 adapters and 16-bit
+// outputs, of rank 136 127 us, of rank 128 100 us.
 template <typename W, typename T, int KS>
 __global__ __launch_bounds__(kThreads, (kResident<KS>)) void lora_expand_kernel(const LoraArgs a, int64_t m0,
                                                                                                 int rows, int most) {
@@ -883,7 +885,7 @@ template <typename W, typename T>
 void expand(const LoraArgs &a, int64_t m0, int rows, hipStream_t stream) {
     const int64_t tiles = (rows + kTile - 1) / kTile;
     // no more workgroups than there can be units; as many as are resident, or where those would have long runs each, more
-    // of shorter ones (long prefill 566 us with 46 units each, 515 with 12; prefill 92 us with 5 units each, 96 with 3)
+    // of shorter ones (long prefill 569 us with 46 units each, 520 with 12, 542 with 3; prefill 84 with 5 units each, 89 with 3)
     const int64_t units = tiles * std::min<int64_t>({kTile, rows, (int64_t)a.L + 1}) * ((a.N + kUnit - 1) / kUnit);
     const int64_t runs = tiles * ((a.N + kUnit - 1) / kUnit) / 12;
     const uint32_t grid = (uint32_t)std::min<int64_t>(units, std::max<int64_t>(256 * kExpandBlocks, std::min<int64_t>(runs, 1 << 20)));

@@ -7,9 +7,12 @@
 // lanes, four scalar reads, one LDS exchange and one barrier.
 //
 // HBM bounds it where there are many rows: 4096 rows of 7168 (fp32 in, bf16 stream, codes) 54 us, 4.9 TB/s, and 20011 rows
-// with a post-norm, a gate, z and codes 319 us, 4.95 TB/s, the rate of a large copy.  4096 rows of 8192 with an fp32
+// with a post-norm, a gate, z and codes 316 us, 5.0 TB/s, the rate of a large copy.  4096 rows of 8192 with an fp32
 // stream and a gate per row take 111 us, 5.4 TB/s.  A few rows wait for one row's chain: one token 5.0 us, 64 rows of
-// 8192 6.0 us, 77 rows of 5003 with two layer norms (five reductions) 8.5 us.  Tried and slower: workgroups that walk
+// 8192 6.0 us, 77 rows of 5003 with two layer norms (five reductions) 8.5 us.  The chain is the reductions, and besides
+// the norms' vectors and the gate, each loaded where it is used, behind the reduction before it and once a chunk,
+// and the stream's store, which the second norm's sums wait for as compiled (they wait for all loads that may be under way
+// there, and stores count with loads).  One row of 16384 takes 7.5 us, of 28672 (four chunks a thread) 11.7 us.  Tried and slower: workgroups that walk
 // rows with the next row's loads ahead, and four rows a workgroup.
 #include "block_internal.hpp"
 
